@@ -27,6 +27,8 @@ Modules:
               FP8 -> FP8 1x128 -> 128x1 re-quantization (all pinned).
     gemm   -- block-scaled GEMM reference for Fprop/Dgrad/Wgrad and the grouped
               variant, plus output rounding to FP32/BF16 (all pinned).
+    ffn    -- gated feed-forward operators: activations, gated product and its
+              gradient, 8-bit integer rows and products (imported on its own).
     study  -- quantization-error study of the scaling rules (per-tensor,
               1x128, 128x128, power-of-2, delayed), built on the pinned
               quantizers; ``python -m oracle.study`` prints the table.

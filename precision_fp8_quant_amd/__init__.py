@@ -1,4 +1,4 @@
-"""Python binding of the fp8q C ABI (include/fp8q.h) for AMD MI355X.
+"""Python binding of the fp8q C ABI (include/fp8q.h, include/fp8q_ffn.h) for AMD MI355X.
 
 Argument marshalling only: every step of quantization and GEMM runs in the
 HIP kernels of ``libfp8q.so``.  torch supplies device memory and the stream.
@@ -14,6 +14,8 @@ Functions keep the C names:
     fp8_gemm_blockscaled_pow2(kind, a, sa, b, sb, pow2_operands) -> c   (power-of-two scales)
     fp8_gemm_blockscaled_grouped(gmap, a, sa, b, sb) -> c
     fp8_requant_1x128_to_128x1(q, scales, mode) -> (q_t, scales_t)
+and, from include/fp8q_ffn.h (module ``ffn``), the gated feed-forward operators fp8_gemm_gated, fp8_gated_backward,
+int8_quant_rows, int8_gemm and int8_gemm_gated.
 FP8 tensors are torch.uint8 holding OCP E4M3FN codes.
 """
 
@@ -305,3 +307,7 @@ def fp8_requant_1x128_to_128x1(q, scales, mode=POW2, q_t=None, scales_t=None, st
     _run(lib.fp8_requant_1x128_to_128x1, dev, stream, q.data_ptr(), rows, cols, _ld(q), scales.data_ptr(), mode,
          q_t.data_ptr(), _ld(q_t), scales_t.data_ptr())
     return q_t, scales_t
+
+
+from .ffn import (ACT_GELU_TANH, ACT_SILU, fp8_gated_backward, fp8_gemm_gated, int8_gemm,  # noqa: E402
+                  int8_gemm_gated, int8_quant_rows)

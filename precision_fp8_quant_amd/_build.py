@@ -17,8 +17,9 @@ LIB_PATH = os.path.join(PKG_DIR, "libfp8q.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-DEVICE_SOURCES = ["quant.hip", "gemm.hip", "gemm_pow2.hip"]
-HOST_SOURCES = ["abi.cpp"]
+DEVICE_SOURCES = ["quant.hip", "gemm.hip", "gemm_pow2.hip", "ffn/fp8_gated.hip", "ffn/int8_gemm.hip",
+                  "ffn/int8_quant.hip", "ffn/gated_backward.hip"]
+HOST_SOURCES = ["abi.cpp", "ffn/abi_ffn.cpp"]
 
 # -ffp-contract=off: the quantizer's scale-multiply-then-round sequence must be
 # exactly the stated FP32 operations (no fused multiply-add formed behind our
@@ -47,11 +48,11 @@ def build(verbose=False, extra_flags=()):
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = []
     for src in DEVICE_SOURCES:
-        obj = os.path.join(BUILD_DIR, src + ".o")
+        obj = os.path.join(BUILD_DIR, src.replace("/", "_") + ".o")
         jobs.append([HIPCC, *COMMON_FLAGS, *DEVICE_FLAGS, *PER_SOURCE_FLAGS.get(src, []), *extra_flags,
                      "-c", os.path.join(CSRC, src), "-o", obj])
     for src in HOST_SOURCES:
-        obj = os.path.join(BUILD_DIR, src + ".o")
+        obj = os.path.join(BUILD_DIR, src.replace("/", "_") + ".o")
         jobs.append([HIPCC, *COMMON_FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj])
     with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
         list(ex.map(lambda c: _run(c, verbose), jobs))
