@@ -31,7 +31,8 @@ DEVICE_FLAGS = ["--offload-arch=gfx950", "-Xclang", "-target-feature", "-Xclang"
 # -amdgpu-mfma-vgpr-form: MFMA results go straight to VGPRs, where the FP32
 # promotion FMAs read them (no v_accvgpr_read copies).  Not for the
 # hardware-scaled GEMM, whose accumulators stay in AGPRs inside the MFMA chain.
-PER_SOURCE_FLAGS = {"gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+PER_SOURCE_FLAGS = {"gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+                    "ffn/fp8_gated.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def _run(cmd, verbose):

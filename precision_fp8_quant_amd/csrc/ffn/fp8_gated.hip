@@ -1,10 +1,16 @@
 // Launcher of the gated product on block-scaled FP8 operands.
 #include "stream_kernel.h"
+#include "tile_kernel.h"
 
 namespace fp8q {
 
+template <int OUT>
+static hipError_t go(const FfnArgs& p, hipStream_t st) {
+  return p.M <= kStreamRows ? launch_stream<false, true, OUT>(p, st) : launch_tile<false, true, OUT>(p, st);
+}
+
 hipError_t launch_fp8_gated(const FfnArgs& p, bool out_bf16, hipStream_t st) {
-  return out_bf16 ? launch_stream<false, true, kOutBF16>(p, st) : launch_stream<false, true, kOutF32>(p, st);
+  return out_bf16 ? go<kOutBF16>(p, st) : go<kOutF32>(p, st);
 }
 
 }  // namespace fp8q

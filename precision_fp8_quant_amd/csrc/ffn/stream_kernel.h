@@ -33,6 +33,7 @@ namespace fp8q {
 typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr int kStreamWaves = 8;
+constexpr int64_t kStreamRows = 64;    // rows of A up to which the weight is streamed
 
 struct Frag {
   u32x4 lo, hi;
