@@ -15,34 +15,16 @@
 
 namespace fp8q {
 
-struct Gate {
-  float s;        // sigma(t)
-  float one_s;    // 1 - sigma(t), not by subtraction: no cancellation where s is near 1
-  float g2;       // g^2, held at 1e4
-};
-
-// e = exp(-|t|) is at most 1, so neither 1 + e nor its reciprocal can
-// overflow; sigma and its complement are r and e r in one order or the other.
-// v_exp_f32 of the rounded product |t| log2(e) is off by about |t| 2^-24 in
-// relative terms, which weighs e / (1 + e) in sigma: below 3e-7 everywhere
-// sigma is not itself under 1e-3.  g^2 is held at 1e4 (|g| = 100, where sigma
-// has long been 0 or 1 for both activations), so that it cannot overflow into
-// 0 * inf.
-__device__ __forceinline__ Gate gate_eval(float g, float c1, float c3) {
-  Gate r;
-  r.g2 = __builtin_fminf(g * g, 1.0e4f);
-  const float t = g * __builtin_fmaf(c3, r.g2, c1);
-  const float e = __builtin_amdgcn_exp2f(-1.44269504088896341f * __builtin_fabsf(t));
-  const float inv = __builtin_amdgcn_rcpf(1.0f + e);
-  const float er = e * inv;
-  r.s = t >= 0.0f ? inv : er;
-  r.one_s = t >= 0.0f ? er : inv;
-  return r;
-}
-
-// act(g) * u
+// act(g) * u.  e = exp(-|t|) is at most 1, so neither 1 + e nor its reciprocal
+// can overflow; sigma is r or e r.  v_exp_f32 of the rounded product
+// |t| log2(e) is off by about |t| 2^-24 in relative terms, which weighs
+// e / (1 + e) in sigma.  g^2 is held at 1e4 (|g| = 100, where sigma has long
+// been 0 or 1 for both activations), so that it cannot overflow into 0 * inf.
 __device__ __forceinline__ float gate_mul(float g, float u, float c1, float c3) {
-  return g * gate_eval(g, c1, c3).s * u;
+  const float t = g * __builtin_fmaf(c3, __builtin_fminf(g * g, 1.0e4f), c1);
+  const float e = __builtin_amdgcn_exp2f(-1.44269504088896341f * __builtin_fabsf(t));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
+  return g * (t >= 0.0f ? r : e * r) * u;
 }
 
 }  // namespace fp8q

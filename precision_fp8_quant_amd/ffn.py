@@ -39,43 +39,42 @@ for _name, _argtypes in SIGNATURES.items():
 
 def _ld(t):
     """Leading dimension in elements; a single row's is its width in whole 16-byte chunks."""
-    if t.shape[0] > 1:
+    rows, cols = t.shape
+    if rows > 1:
         return t.stride(0)
     per = 16 // t.element_size()
-    return max(_cdiv(t.shape[1], per), 1) * per
+    return max(cols + -cols % per, per)
 
 
 def _empty_rows16(rows, cols, dtype, device):
     """A [rows][cols] tensor whose rows start at multiples of 16 bytes."""
-    per = 16 // dtype.itemsize
-    ld = _cdiv(cols, per) * per
-    t = torch.empty((rows, ld), dtype=dtype, device=device)
-    return t if ld == cols else t[:, :cols]
+    pad = -cols % (16 // dtype.itemsize)
+    t = torch.empty((rows, cols + pad), dtype=dtype, device=device)
+    return t[:, :cols] if pad else t
 
 
 def _out(t, name, dtype, shape, device):
     """The caller's output tensor, checked, or a new one."""
-    if t is None:
-        if dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
-        return _empty_rows16(*shape, dtype, device)
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    return _expect(t, name, t.dtype, shape, device)
+    if t is not None:
+        dtype = t.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
+    return _empty_rows16(*shape, dtype, device) if t is None else _expect(t, name, dtype, shape, device)
 
 
 def _ints(t, name):
-    """An 8-bit integer operand, whose rows the library reads in whole 16-byte chunks."""
+    """Leading dimension of an 8-bit integer operand, whose rows the library reads in whole 16-byte chunks."""
     _rowmajor(t, name)
     if t.dtype != torch.int8:
         raise TypeError(f"{name} must be torch.int8, got {t.dtype}")
     rows, cols = t.shape
-    if rows and cols and _ld(t) % 16 == 0:         # any other leading dimension is the ABI's FP8Q_ERR_ALIGN
-        need = t.storage_offset() + (rows - 1) * _ld(t) + _cdiv(cols, 16) * 16
-        if need > t.untyped_storage().nbytes():
+    ld = _ld(t)
+    # any other leading dimension is the ABI's FP8Q_ERR_ALIGN
+    if cols % 16 and rows and ld % 16 == 0:
+        if t.storage_offset() + (rows - 1) * ld + cols + -cols % 16 > t.untyped_storage().nbytes():
             raise ValueError(f"{name}'s rows are read in whole 16-byte chunks: the storage must hold the last row up to "
                              "the next multiple of 16 bytes")
-    return t
+    return ld
 
 
 def fp8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bfloat16, h=None, gu=None,
@@ -153,7 +152,7 @@ def int8_quant_rows(x, q=None, scales=None, stream=None):
 
 def int8_gemm(a, a_scales, b, b_scales, bias=None, out_dtype=torch.bfloat16, c=None, stream=None):
     """C[M][N] = a_scales[m] * b_scales[n] * (A . B^T) (+ bias[n]) from 8-bit integers a [M][K] and b [N][K]."""
-    a, b = _ints(a, "a"), _ints(b, "b")
+    lda, ldb = _ints(a, "a"), _ints(b, "b")
     (m, k), n, dev = a.shape, b.shape[0], a.device
     if b.shape[1] != k:
         raise ValueError("a and b disagree on K")
@@ -163,7 +162,7 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, out_dtype=torch.bfloat16, c=N
     if bias is not None:
         _expect(bias, "bias", torch.float32, (n,), dev, dense=True)
     c = _out(c, "c", out_dtype, (m, n), dev)
-    _run(lib.int8_gemm, dev, stream, m, n, k, a.data_ptr(), _ld(a), a_scales.data_ptr(), b.data_ptr(), _ld(b),
+    _run(lib.int8_gemm, dev, stream, m, n, k, a.data_ptr(), lda, a_scales.data_ptr(), b.data_ptr(), ldb,
          b_scales.data_ptr(), None if bias is None else bias.data_ptr(), c.data_ptr(), _dtype_code(c), _ld(c))
     return c
 
@@ -171,7 +170,7 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, out_dtype=torch.bfloat16, c=N
 def int8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bfloat16, h=None, stream=None):
     """h[M][F] = act(g) * u with g and u the int8_gemm products of a [M][K] and the stacked gate and up weights
     b [2F][K]."""
-    a, b = _ints(a, "a"), _ints(b, "b")
+    lda, ldb = _ints(a, "a"), _ints(b, "b")
     (m, k), n2, dev = a.shape, b.shape[0], a.device
     if b.shape[1] != k:
         raise ValueError("a and b disagree on K")
@@ -181,6 +180,6 @@ def int8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bflo
     _expect(a_scales, "a_scales", torch.float32, (m,), dev, dense=True)
     _expect(b_scales, "b_scales", torch.float32, (n2,), dev, dense=True)
     h = _out(h, "h", out_dtype, (m, n2 // 2), dev)
-    _run(lib.int8_gemm_gated, dev, stream, act, m, n2 // 2, k, a.data_ptr(), _ld(a), a_scales.data_ptr(),
-         b.data_ptr(), _ld(b), b_scales.data_ptr(), h.data_ptr(), _dtype_code(h), _ld(h))
+    _run(lib.int8_gemm_gated, dev, stream, act, m, n2 // 2, k, a.data_ptr(), lda, a_scales.data_ptr(),
+         b.data_ptr(), ldb, b_scales.data_ptr(), h.data_ptr(), _dtype_code(h), _ld(h))
     return h
