@@ -8,14 +8,17 @@
 // scales, as in gemm_kernel.h).
 //
 // For M rows the weight's K N bytes are read once and feed 2 M operations
-// each, so below some tens of rows the memory bounds the product and all that
-// counts is how many bytes of B are in flight.  A workgroup of 8 waves owns
-// 16 MF rows x 16 columns (gated: of both projections); the waves share out K
-// in runs of UNROLL 128-byte groups, and each loads its B bytes from global
-// memory directly in fragment order: no LDS and no barrier stands between the
-// loads and the matrix instructions.  The waves' partial sums meet in LDS
-// once, at the end, and are added in a fixed order, so the result does not
-// depend on timing.
+// each, so for few rows the memory bounds the product and all that counts is
+// how many bytes of B are in flight.  A workgroup of 8 or 16 waves owns 16 MF
+// rows x 16 NF columns (gated: of both projections); the waves share out K in
+// contiguous runs, and each loads its B bytes from global memory directly in
+// fragment order, UNROLL groups before the first is used: no LDS and no barrier
+// stands between the loads and the matrix instructions.  The waves' partial
+// sums meet in LDS once, at the end, and are added in a fixed order, so the
+// result does not depend on timing.  Measured on one row: int8 gated
+// 18432x7168 47.3 us (5.6 TB/s of weight), int8 7168x18432 26.0 us (5.1), FP8
+// gated 18432x7168 47.3 us (5.6); the first 63.6 with the loads left to the
+// compiler's order (three in flight) and the scales fetched in the epilogue.
 //
 // The matrix instruction takes the B fragment as source A (16 rows of N) and
 // the A fragment as source B (16 rows of M), so a lane's four results are four
@@ -25,15 +28,13 @@
 #pragma once
 
 #include "../gemm_kernel.h"
+#include "bf16.h"
 #include "ffn_launch.h"
 #include "gate_act.h"
 
 namespace fp8q {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
-
-constexpr int kStreamWaves = 8;
-constexpr int64_t kStreamRows = 64;    // rows of A up to which the weight is streamed
 
 struct Frag {
   u32x4 lo, hi;
@@ -71,23 +72,23 @@ __device__ __forceinline__ Frag load_frag(const uint8_t* row, int64_t k, int64_t
   return f;
 }
 
-template <bool INT8, bool GATED, int MF, int OUT>
-__global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(FfnArgs p) {
+template <bool INT8, bool GATED, int MF, int NF, int WAVES, int UNROLL, int OUT>
+__global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
   constexpr int NP = GATED ? 2 : 1;               // projections
-  constexpr int UNROLL = MF <= 2 ? 4 : 2;         // 128-byte groups loaded before the first is used
   typedef typename std::conditional<INT8, v4i, v4f>::type acc_t;
-  __shared__ acc_t part[kStreamWaves][NP * MF][64];
+  __shared__ acc_t part[WAVES][NP * MF][64];
+  __shared__ float s_sa[16 * MF], s_sb[NP * NF * 16], s_bias[NP * NF * 16];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lq = lane >> 4;
-  const int64_t ntiles = (p.N + 15) >> 4;
-  const int64_t n0 = (blockIdx.x % ntiles) * 16;
+  const int64_t ntiles = (p.N + 16 * NF - 1) / (16 * NF);
+  const int64_t n0 = (blockIdx.x % ntiles) * (16 * NF);
   const int64_t m0 = (blockIdx.x / ntiles) * (16 * MF);
 
   // Rows past the end repeat the last one: their products are not stored.
   const uint8_t* arow[MF];
-  const uint8_t* brow[NP];
+  const uint8_t* brow[NP][NF];
   int64_t mrow[MF];
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
@@ -95,147 +96,230 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(FfnArgs p) {
     mrow[i] = m < p.M ? m : p.M - 1;
     arow[i] = p.a + mrow[i] * p.lda + 16 * lq;
   }
-  {
-    const int64_t n = n0 + lr < p.N ? n0 + lr : p.N - 1;
 #pragma unroll
-    for (int b = 0; b < NP; ++b) brow[b] = p.b + (b * p.N + n) * p.ldb + 16 * lq;
+  for (int f = 0; f < NF; ++f) {
+    const int64_t c = n0 + 16 * f + lr;
+    const int64_t n = c < p.N ? c : p.N - 1;
+#pragma unroll
+    for (int b = 0; b < NP; ++b) brow[b][f] = p.b + (b * p.N + n) * p.ldb + 16 * lq;
   }
 
-  acc_t acc[NP][MF];
+  acc_t acc[NP][NF][MF];
 #pragma unroll
   for (int b = 0; b < NP; ++b)
 #pragma unroll
-    for (int i = 0; i < MF; ++i) acc[b][i] = acc_t{0, 0, 0, 0};
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int i = 0; i < MF; ++i) acc[b][f][i] = acc_t{0, 0, 0, 0};
 
   const int64_t KG = (p.K + 127) >> 7;            // FP8: K is a multiple of 128
   const int64_t kfull = p.K >> 7;                 // groups wholly inside K
 
-  auto use = [&](const Frag (&fa)[MF], const Frag (&fb)[NP], int64_t g) {
-    if constexpr (INT8) {
-#pragma unroll
-      for (int b = 0; b < NP; ++b)
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-          acc[b][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, fb[b].lo),
-                                                            __builtin_bit_cast(v4i, fa[i].lo), acc[b][i], 0, 0, 0);
-          acc[b][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, fb[b].hi),
-                                                            __builtin_bit_cast(v4i, fa[i].hi), acc[b][i], 0, 0, 0);
-        }
-    } else {
-      const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int b = 0; b < NP; ++b) {
-        const float sb = p.sb[((b * p.N + n0) >> 7) * KG + g];
-        const v8i vb = {int(fb[b].lo.x), int(fb[b].lo.y), int(fb[b].lo.z), int(fb[b].lo.w),
-                        int(fb[b].hi.x), int(fb[b].hi.y), int(fb[b].hi.z), int(fb[b].hi.w)};
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-          const v8i va = {int(fa[i].lo.x), int(fa[i].lo.y), int(fa[i].lo.z), int(fa[i].lo.w),
-                          int(fa[i].hi.x), int(fa[i].hi.y), int(fa[i].hi.z), int(fa[i].hi.w)};
-          const v4f d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, zero, 0, 0, 0, 0, 0, 0);
-          const float c = p.sa[g * p.M + mrow[i]] * sb;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[b][i][j] = __builtin_fmaf(d[j], c, acc[b][i][j]);
-        }
-      }
-    }
+  struct Group {
+    Frag a[MF], b[NP][NF];
+    float sa[MF], sb[NP];                         // FP8: this group's scales
   };
-
-  int64_t g = wave * UNROLL;
-  for (; g + UNROLL <= kfull; g += kStreamWaves * UNROLL) {
-    Frag fa[UNROLL][MF], fb[UNROLL][NP];
-#pragma unroll
-    for (int s = 0; s < UNROLL; ++s) {
-#pragma unroll
-      for (int b = 0; b < NP; ++b) fb[s][b] = load_frag<false, false>(brow[b], (g + s) * 128, p.K);
-#pragma unroll
-      for (int i = 0; i < MF; ++i) fa[s][i] = load_frag<false, false>(arow[i], (g + s) * 128, p.K);
-    }
-#pragma unroll
-    for (int s = 0; s < UNROLL; ++s) use(fa[s], fb[s], g + s);
-  }
-  // the run that holds the last whole groups and the group that reaches beyond K
-  for (int64_t e = g + UNROLL < KG ? g + UNROLL : KG; g < e; ++g) {
-    Frag fa[MF], fb[NP];
+  auto load = [&](auto tail, Group& x, int64_t g) {
+    constexpr bool TAIL = decltype(tail)::value;
     const int64_t left = p.K - 16 * lq;           // K as seen from this lane's first chunk
-#pragma unroll
-    for (int b = 0; b < NP; ++b) fb[b] = load_frag<true, false>(brow[b], g * 128, left);
-#pragma unroll
-    for (int i = 0; i < MF; ++i) fa[i] = load_frag<true, true>(arow[i], g * 128, left);
-    use(fa, fb, g);
-  }
-
-#pragma unroll
-  for (int b = 0; b < NP; ++b)
-#pragma unroll
-    for (int i = 0; i < MF; ++i) part[wave][b * MF + i][lane] = acc[b][i];
-  __syncthreads();
-
-  // Thread t adds the 8 waves' parts of fragment t/64, lane t%64, and finishes
-  // four columns of one row.
-  for (int f = wave; f < MF; f += kStreamWaves) {
-    const int64_t m = m0 + 16 * f + lr;
-    const int64_t n = n0 + 4 * lq;
-    if (m >= p.M || n >= p.N) continue;
-    acc_t sum[NP];
-#pragma unroll
-    for (int b = 0; b < NP; ++b) {
-      sum[b] = part[0][b * MF + f][lane];
-#pragma unroll
-      for (int w = 1; w < kStreamWaves; ++w) sum[b] += part[w][b * MF + f][lane];
-    }
-    const int cols = p.N - n < 4 ? int(p.N - n) : 4;
-    const float sa = (INT8 && p.K > 0) ? p.sa[m] : 1.0f;
-    float y[NP][4], out[4];
 #pragma unroll
     for (int b = 0; b < NP; ++b)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        y[b][j] = float(sum[b][j]);
-        if constexpr (INT8) y[b][j] *= (p.K > 0 && j < cols) ? sa * p.sb[b * p.N + n + j] : 0.0f;
-      }
+      for (int f = 0; f < NF; ++f) x.b[b][f] = load_frag<TAIL, false>(brow[b][f], g * 128, left);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (GATED) out[j] = gate_mul(y[0][j], y[1][j], p.act_c1, p.act_c3);
-      else out[j] = (p.bias && j < cols) ? y[0][j] + p.bias[n + j] : y[0][j];
+    for (int i = 0; i < MF; ++i) x.a[i] = load_frag<TAIL, TAIL>(arow[i], g * 128, left);
+    if constexpr (!INT8) {
+#pragma unroll
+      for (int i = 0; i < MF; ++i) x.sa[i] = p.sa[g * p.M + mrow[i]];
+#pragma unroll
+      for (int b = 0; b < NP; ++b) x.sb[b] = p.sb[((b * p.N + n0) >> 7) * KG + g];
     }
-    auto store = [&](void* base, int64_t ld, int64_t col, const float (&v)[4]) {
-      if constexpr (OUT == kOutBF16) {
-        uint16_t* dst = static_cast<uint16_t*>(base) + m * ld + col;
-        if (cols == 4) {
-          *reinterpret_cast<uint2*>(dst) = uint2{bf16_rne_bits(v[0]) | (bf16_rne_bits(v[1]) << 16),
-                                                 bf16_rne_bits(v[2]) | (bf16_rne_bits(v[3]) << 16)};
-        } else {
-          for (int j = 0; j < cols; ++j) dst[j] = uint16_t(bf16_rne_bits(v[j]));
+  };
+  auto use = [&](const Group& x) {
+    if constexpr (INT8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int b = 0; b < NP; ++b)
+#pragma unroll
+          for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+              acc[b][f][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                  __builtin_bit_cast(v4i, h ? x.b[b][f].hi : x.b[b][f].lo),
+                  __builtin_bit_cast(v4i, h ? x.a[i].hi : x.a[i].lo), acc[b][f][i], 0, 0, 0);
+    } else {
+      const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+      auto v = [](const Frag& f) {
+        return v8i{int(f.lo.x), int(f.lo.y), int(f.lo.z), int(f.lo.w), int(f.hi.x), int(f.hi.y), int(f.hi.z), int(f.hi.w)};
+      };
+#pragma unroll
+      for (int b = 0; b < NP; ++b)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+          for (int i = 0; i < MF; ++i) {
+            const v4f d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v(x.b[b][f]), v(x.a[i]), zero, 0, 0, 0, 0, 0, 0);
+            const float c = x.sa[i] * x.sb[b];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[b][f][i][j] = __builtin_fmaf(d[j], c, acc[b][f][i][j]);
+          }
+    }
+  };
+
+  // What the epilogue multiplies and adds is on its way before the weight, one
+  // value of each kind per thread (past the end: the last row's or column's).
+  const int tid = threadIdx.x;
+  float my_sa = 0.0f, my_sb = 0.0f, my_bias = 0.0f;
+  if constexpr (INT8) {
+    if (p.K > 0 && tid < 16 * MF) my_sa = p.sa[m0 + tid < p.M ? m0 + tid : p.M - 1];
+    if (tid < NP * NF * 16) {
+      const int64_t c = n0 + tid % (NF * 16), n = c < p.N ? c : p.N - 1;
+      if (p.K > 0) my_sb = p.sb[tid / (NF * 16) * p.N + n];
+      if (!GATED && p.bias) my_bias = p.bias[n];
+    }
+  }
+
+  // This wave's contiguous share of the groups: [g, whole) inside K, and up to
+  // `end` the group that reaches beyond it.
+  int64_t g = KG * wave / WAVES;
+  const int64_t end = KG * (wave + 1) / WAVES;
+  const int64_t whole = end < kfull ? end : kfull;
+  // `n` groups (n <= UNROLL): all loads are issued before the first is used
+  auto run = [&](auto full, int n) {
+    Group x[UNROLL];
+#pragma unroll
+    for (int s = 0; s < UNROLL; ++s)
+      if (full || s < n) load(std::false_type{}, x[s], g + s);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < UNROLL; ++s)
+      if (full || s < n) use(x[s]);
+  };
+  for (; g + UNROLL <= whole; g += UNROLL) run(std::true_type{}, UNROLL);
+  if (g < whole) run(std::false_type{}, int(whole - g));
+  if (end > kfull) {
+    Group x;
+    load(std::true_type{}, x, kfull);
+    use(x);
+  }
+
+  if constexpr (INT8) {
+    if (tid < 16 * MF) s_sa[tid] = my_sa;
+    if (tid < NP * NF * 16) {
+      s_sb[tid] = my_sb;
+      s_bias[tid] = my_bias;
+    }
+  }
+  // The waves' parts meet in LDS, 16 columns at a time.
+  const int64_t m = m0 + 16 * wave + lr;
+#pragma unroll
+  for (int nf = 0; nf < NF; ++nf) {
+    if (nf) __syncthreads();
+#pragma unroll
+    for (int b = 0; b < NP; ++b)
+#pragma unroll
+      for (int i = 0; i < MF; ++i) part[wave][b * MF + i][lane] = acc[b][nf][i];
+    __syncthreads();
+    // Wave f adds the parts of row fragment f; a lane finishes four columns of
+    // one row.
+    if (wave < MF && m < p.M && n0 + 16 * nf + 4 * lq < p.N) {
+      const int64_t n = n0 + 16 * nf + 4 * lq;
+      acc_t sum[NP];
+#pragma unroll
+      for (int b = 0; b < NP; ++b) {
+        sum[b] = part[0][b * MF + wave][lane];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) sum[b] += part[w][b * MF + wave][lane];
+      }
+      const int cols = p.N - n < 4 ? int(p.N - n) : 4;
+      float y[NP][4], out[4];
+#pragma unroll
+      for (int b = 0; b < NP; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          y[b][j] = float(sum[b][j]);
+          if constexpr (INT8) y[b][j] *= s_sa[16 * wave + lr] * s_sb[b * (NF * 16) + 16 * nf + 4 * lq + j];
         }
-      } else {
-        float* dst = static_cast<float*>(base) + m * ld + col;
-        if (cols == 4) *reinterpret_cast<v4f*>(dst) = v4f{v[0], v[1], v[2], v[3]};
-        else
-          for (int j = 0; j < cols; ++j) dst[j] = v[j];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (GATED) out[j] = gate_mul(y[0][j], y[1][j], p.act_c1, p.act_c3);
+        else out[j] = p.bias ? y[0][j] + s_bias[16 * nf + 4 * lq + j] : y[0][j];
       }
-    };
-    store(p.c, p.ldc, n, out);
-    if constexpr (GATED)
-      if (p.gu) {
-        store(p.gu, p.ldgu, n, y[0]);
-        store(p.gu, p.ldgu, p.N + n, y[1]);
-      }
+      auto store = [&](void* base, int64_t ld, int64_t col, const float (&v)[4]) {
+        if constexpr (OUT == kOutBF16) {
+          uint16_t* dst = static_cast<uint16_t*>(base) + m * ld + col;
+          const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
+          if (cols == 4) {
+            *reinterpret_cast<uint2*>(dst) = uint2{lo, hi};
+          } else {
+            dst[0] = uint16_t(lo);
+            if (cols > 1) dst[1] = uint16_t(lo >> 16);
+            if (cols > 2) dst[2] = uint16_t(hi);
+          }
+        } else {
+          float* dst = static_cast<float*>(base) + m * ld + col;
+          if (cols == 4) {
+            *reinterpret_cast<v4f*>(dst) = v4f{v[0], v[1], v[2], v[3]};
+          } else {
+            dst[0] = v[0];
+            if (cols > 1) dst[1] = v[1];
+            if (cols > 2) dst[2] = v[2];
+          }
+        }
+      };
+      store(p.c, p.ldc, n, out);
+      if constexpr (GATED)
+        if (p.gu) {
+          store(p.gu, p.ldgu, n, y[0]);
+          store(p.gu, p.ldgu, p.N + n, y[1]);
+        }
+    }
   }
 }
 
-template <bool INT8, bool GATED, int MF, int OUT>
+template <bool INT8, bool GATED, int OUT, int MF, int NF, int WAVES, int UNROLL>
 static hipError_t launch_stream_cfg(const FfnArgs& p, hipStream_t st) {
-  const int64_t tiles = ((p.N + 15) / 16) * ((p.M + 16 * MF - 1) / (16 * MF));
-  hipLaunchKernelGGL((stream_kernel<INT8, GATED, MF, OUT>), dim3(unsigned(tiles)), dim3(kStreamWaves * 64), 0, st, p);
+  const int64_t tiles = ((p.N + 16 * NF - 1) / (16 * NF)) * ((p.M + 16 * MF - 1) / (16 * MF));
+  hipLaunchKernelGGL((stream_kernel<INT8, GATED, MF, NF, WAVES, UNROLL, OUT>), dim3(unsigned(tiles)), dim3(WAVES * 64),
+                     0, st, p);
   return hipGetLastError();
 }
 
+// Whether streaming beats the LDS tiles (tile_kernel.h).  Streaming takes time in
+// proportion to the weight's bytes and, beyond 16 rows, to the rows of A that
+// every wave fetches beside them (microseconds per 128-deep K-group and row of
+// B: 3.5e-5 up to 32 rows, 5.1e-5 up to 64); the tiles take at least 0.53 per
+// group however few they are.  Measured (us, streaming / tiles): int8 gated
+// 18432x7168, 32 rows 69 / 63, 64 rows 94 / 67; int8 7168x18432, 32 rows
+// 36 / 109, 64 rows 53 / 109; FP8 gated 2048x7168, 64 rows 23 / 31.
+template <bool GATED>
+static bool streams(const FfnArgs& p) {
+  const int64_t brows = GATED ? 2 * p.N : p.N;
+  return p.M <= 16 || (p.M <= 32 && brows <= 15000) || (p.M <= 64 && brows <= 10400);
+}
+
+// 16 waves where there are fewer workgroups than CUs (FP8 gated 16x2048x7168
+// 12.2 us a call against 12.5), 8 otherwise (int8 1x7168x18432 26.0 against
+// 29.8).  Two column fragments per wave halve what a plain product fetches of A
+// (int8 16x7168x18432 29.0 against 36.8), if they leave enough workgroups; a
+// gated one has its two projections already (FP8 16x18432x7168 56.8 with one,
+// 58.9 with two).
 template <bool INT8, bool GATED, int OUT>
 static hipError_t launch_stream(const FfnArgs& p, hipStream_t st) {
-  if (p.M <= 16) return launch_stream_cfg<INT8, GATED, 1, OUT>(p, st);
-  if (p.M <= 32) return launch_stream_cfg<INT8, GATED, 2, OUT>(p, st);
-  return launch_stream_cfg<INT8, GATED, 4, OUT>(p, st);
+  const bool few = (p.N + 15) / 16 <= 256;
+  if constexpr (!GATED) {
+    if (p.M > 4 && (p.N + 31) / 32 >= 192) {
+      if (p.M <= 16) return launch_stream_cfg<INT8, GATED, OUT, 1, 2, 8, 2>(p, st);
+      if (p.M <= 32) return launch_stream_cfg<INT8, GATED, OUT, 2, 2, 8, 2>(p, st);
+      return launch_stream_cfg<INT8, GATED, OUT, 4, 2, 8, 2>(p, st);
+    }
+  }
+  if (p.M <= 16) return few ? launch_stream_cfg<INT8, GATED, OUT, 1, 1, 16, 4>(p, st)
+                            : launch_stream_cfg<INT8, GATED, OUT, 1, 1, 8, 4>(p, st);
+  if (p.M <= 32) return few ? launch_stream_cfg<INT8, GATED, OUT, 2, 1, 16, 2>(p, st)
+                            : launch_stream_cfg<INT8, GATED, OUT, 2, 1, 8, 2>(p, st);
+  return launch_stream_cfg<INT8, GATED, OUT, 4, 1, 8, 2>(p, st);
 }
 
 }  // namespace fp8q
