@@ -286,17 +286,18 @@ static hipError_t launch_stream_cfg(const FfnArgs& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Whether streaming beats the LDS tiles (tile_kernel.h).  Streaming takes time in
-// proportion to the weight's bytes and, beyond 16 rows, to the rows of A that
-// every wave fetches beside them (microseconds per 128-deep K-group and row of
-// B: 3.5e-5 up to 32 rows, 5.1e-5 up to 64); the tiles take at least 0.53 per
-// group however few they are.  Measured (us, streaming / tiles): int8 gated
-// 18432x7168, 32 rows 69 / 63, 64 rows 94 / 67; int8 7168x18432, 32 rows
-// 36 / 109, 64 rows 53 / 109; FP8 gated 2048x7168, 64 rows 23 / 31.
+// Whether streaming beats the LDS tiles (tile_kernel.h).  Beyond 16 rows every
+// wave fetches as much of A beside its weight again, and streaming takes
+// (microseconds per 128-deep K-group and row of B) 3.5e-5 up to 32 rows and
+// 5.1e-5, but no less than 0.41 per group, up to 64; the tiles take 0.33 per
+// group with few rows of B, 0.44 with 7168, and 3e-5 per row with many.
+// Measured (us, streaming / tiles): 32 rows, 7168 rows of B by 18432 36 / 57,
+// 36864 by 7168 69 / 63, 4096 by 7168 16 / 17; 64 rows, the same 53 / 64,
+// 94 / 67, 23 / 18.5.
 template <bool GATED>
 static bool streams(const FfnArgs& p) {
   const int64_t brows = GATED ? 2 * p.N : p.N;
-  return p.M <= 16 || (p.M <= 32 && brows <= 15000) || (p.M <= 64 && brows <= 10400);
+  return p.M <= 16 || (p.M <= 32 && brows <= 24000) || (p.M <= 64 && brows > 5500 && brows <= 8600);
 }
 
 // 16 waves where there are fewer workgroups than CUs (FP8 gated 16x2048x7168

@@ -19,6 +19,8 @@
 //    scales are applied once, in the epilogue.
 //  * Block-scaled FP8: a group's A-row and block scales travel with its stage
 //    (4-byte LDS DMA), so nothing in the loop waits on a register load.
+//  * KW teams of waves in one workgroup may take a tile's K-groups in turn, each
+//    with its own stages; their sums meet in LDS at the end, in a fixed order.
 //  * Any M, N (integers) and K (integers): a tile's rows past the end repeat the
 //    last valid row (their products are not stored), so every DMA address is
 //    inside its operand; in the group that reaches beyond K the A tile's bytes
@@ -34,10 +36,10 @@ namespace fp8q {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 
-template <bool INT8, bool GATED, int BM, int BN, int WM, int PF, int STAGES, int OUT>
-__global__ __launch_bounds__(WM * (BN / (32 * PF)) * 64) void tile_kernel(FfnArgs p) {
+template <bool INT8, bool GATED, int BM, int BN, int WM, int PF, int STAGES, int KW, int OUT>
+__global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(FfnArgs p) {
   constexpr int WN = BN / (32 * PF);    // waves along B's rows
-  constexpr int NW = WM * WN;
+  constexpr int NW = WM * WN;           // waves per team; KW teams take the K-groups in turn
   constexpr int TM = BM / WM;           // wave tile rows
   constexpr int SM = TM / 16;           // 16-row subtiles per wave
   constexpr int PC = 16 * PF;           // columns per panel
@@ -53,13 +55,15 @@ __global__ __launch_bounds__(WM * (BN / (32 * PF)) * 64) void tile_kernel(FfnArg
   static_assert(INT8 || (128 % CN == 0 && BM / 64 <= NW), "FP8: a tile in one scale block, one A-scale DMA a wave");
   constexpr int ESZ = OUT == kOutBF16 ? 2 : 4;
   constexpr int PITCH = PC * ESZ + 16;           // bytes per staged output row
-  constexpr int LOOP_LDS = STAGES * STAGE;
+  constexpr int LOOP_LDS = KW * STAGES * STAGE;
   constexpr int EPI_LDS = NW * TM * PITCH;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[LOOP_LDS > EPI_LDS ? LOOP_LDS : EPI_LDS];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[LOOP_LDS > EPI_LDS ? LOOP_LDS : EPI_LDS];
 
-  const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = threadIdx.x & 63;
+  const int team = KW > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / NW : 0;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) - team * NW;     // within the team
+  const int tid = threadIdx.x - team * (NW * 64);
+  uint8_t* const smem = lds + team * (STAGES * STAGE);
   const int wm = wave / WN, wn = wave % WN;
   const int lr = lane & 15, lq = lane >> 4;
 
@@ -161,8 +165,10 @@ __global__ __launch_bounds__(WM * (BN / (32 * PF)) * 64) void tile_kernel(FfnArg
 #pragma unroll
       for (int c = 0; c < PF; ++c) acc[a][b][c] = acc_t{0, 0, 0, 0};
 
-  // Groups 0 .. STAGES-2 are under way before the loop, group g + STAGES-1 is
-  // requested while group g is computed, into the stage that group g-1 has left.
+  // Team `team` computes groups team, team + KW, ... in its own ring of stages
+  // (below, "group g" is a team's g-th).  Groups 0 .. STAGES-2 are under way
+  // before the loop, group g + STAGES-1 is requested while group g is computed,
+  // into the stage that group g-1 has left.
   // Loads return in order, so a wave's part of group g has landed once at most
   // the STAGES-2 younger groups' DMAs are outstanding; the barrier then says so
   // for every wave, and that every wave is done with group g-1.  Past the last
@@ -170,7 +176,11 @@ __global__ __launch_bounds__(WM * (BN / (32 * PF)) * 64) void tile_kernel(FfnArg
   // land in stages that are not read any more, before the epilogue's barrier.
   constexpr int YOUNGER = (STAGES - 2) * (A_DMA + B_DMA);
   static_assert(STAGES >= 2 && YOUNGER < 64, "vmcnt holds six bits");
-  auto clampg = [&](int64_t g) { return g < KG ? g : KG - 1; };
+  auto clampg = [&](int64_t i) {                  // K-group of this team's i-th turn
+    const int64_t g = i * KW + team;
+    return g < KG ? g : KG - 1;
+  };
+  const int64_t turns = (KG + KW - 1) / KW;
   if (KG > 0) {
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) {
@@ -181,7 +191,7 @@ __global__ __launch_bounds__(WM * (BN / (32 * PF)) * 64) void tile_kernel(FfnArg
   }
 
   int stage = 0;
-  for (int64_t g = 0; g < KG; ++g) {
+  for (int64_t g = 0; g < turns; ++g) {
     __builtin_amdgcn_s_waitcnt(0x0F70 | (YOUNGER & 15) | ((YOUNGER >> 4) << 14));    // vmcnt(YOUNGER)
     __syncthreads();
     const int64_t gn = clampg(g + STAGES - 1);
@@ -190,18 +200,20 @@ __global__ __launch_bounds__(WM * (BN / (32 * PF)) * 64) void tile_kernel(FfnArg
     uint8_t* const ta = smem + stage * STAGE;
     const uint8_t* const tb = ta + A_BYTES;
     if constexpr (INT8) {
-      if (g + 1 == KG && (p.K & 127)) {            // block-uniform
+      if (g + 1 == turns && (p.K & 127)) {         // block-uniform
         const int k = int(p.K & 127);
-        for (int w = tid; w < BM * 32; w += NW * 64) {           // dword w%32 of row w/32
-          const int row = w >> 5, byte = (w & 31) * 4;
-          if (byte + 4 > k) {
-            uint32_t* dst = reinterpret_cast<uint32_t*>(ta + lds_off(row, byte >> 4) + (byte & 15));
-            *dst = byte >= k ? 0u : *dst & ((1u << (8 * (k - byte))) - 1u);
+        if (KW == 1 || g * KW + team == KG - 1)
+          for (int w = tid; w < BM * 32; w += NW * 64) {         // dword w%32 of row w/32
+            const int row = w >> 5, byte = (w & 31) * 4;
+            if (byte + 4 > k) {
+              uint32_t* dst = reinterpret_cast<uint32_t*>(ta + lds_off(row, byte >> 4) + (byte & 15));
+              *dst = byte >= k ? 0u : *dst & ((1u << (8 * (k - byte))) - 1u);
+            }
           }
-        }
         __syncthreads();
       }
     }
+    if (KW > 1 && g * KW + team >= KG) break;      // the last turn has fewer groups than teams; no barrier is left in it
 
     v8i af[SM];
     v8i bf[3];
@@ -258,8 +270,29 @@ __global__ __launch_bounds__(WM * (BN / (32 * PF)) * 64) void tile_kernel(FfnArg
     }
     stage = stage + 1 == STAGES ? 0 : stage + 1;
   }
-  wait_vmem_all();                               // the epilogue reuses the stages
+  wait_vmem_all();                               // what follows reuses the stages
   __syncthreads();
+
+  // The teams' sums meet in the first one's registers, in the teams' order.
+  if constexpr (KW > 1) {
+    constexpr int FR = SM * 2 * PF;
+    static_assert((KW - 1) * NW * FR * 1024 <= int(sizeof(lds)), "the teams' sums fit the stages");
+    acc_t* const red = reinterpret_cast<acc_t*>(lds) + lane;
+    if (team > 0) {
+#pragma unroll
+      for (int i = 0; i < FR; ++i)
+        red[(((team - 1) * NW + wave) * FR + i) * 64] = acc[i / (2 * PF)][i / PF % 2][i % PF];
+    }
+    __syncthreads();
+    if (team == 0) {
+#pragma unroll
+      for (int k = 0; k < KW - 1; ++k)
+#pragma unroll
+        for (int i = 0; i < FR; ++i) acc[i / (2 * PF)][i / PF % 2][i % PF] += red[((k * NW + wave) * FR + i) * 64];
+    }
+    __syncthreads();                             // the output tile is staged over the sums
+    if (team > 0) return;
+  }
 
   // ---- epilogue --------------------------------------------------------------
   // As in gemm_kernel.h the tile leaves through LDS, one panel per wave at a
@@ -369,45 +402,65 @@ __global__ __launch_bounds__(WM * (BN / (32 * PF)) * 64) void tile_kernel(FfnArg
   }
 }
 
-template <bool INT8, bool GATED, int OUT, int BM, int BN, int WM, int PF, int STAGES>
+template <bool INT8, bool GATED, int OUT, int BM, int BN, int WM, int PF, int STAGES, int KW>
 static hipError_t launch_tile_cfg(const FfnArgs& p, hipStream_t st) {
   constexpr int CN = GATED ? BN / 2 : BN;
   const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.N + CN - 1) / CN);
-  hipLaunchKernelGGL((tile_kernel<INT8, GATED, BM, BN, WM, PF, STAGES, OUT>), dim3(unsigned(tiles)),
-                     dim3(WM * (BN / (32 * PF)) * 64), 0, st, p);
+  hipLaunchKernelGGL((tile_kernel<INT8, GATED, BM, BN, WM, PF, STAGES, KW, OUT>), dim3(unsigned(tiles)),
+                     dim3(KW * WM * (BN / (32 * PF)) * 64), 0, st, p);
   return hipGetLastError();
 }
 
 template <bool INT8, bool GATED, int OUT>
 static hipError_t launch_tile(const FfnArgs& p, hipStream_t st) {
-  // Four tile shapes (BM x BN, waves of TM x 32 PF):
-  //   256x256  8 waves of 64x128, 1 workgroup per CU
-  //   128x128  4 waves of 64x64, 2
-  //   64x128   4 waves of 32x64, 2
-  //   64x64    4 waves of 16x64, 2
+  // Five tilings (BM x BN by KW teams, waves of TM x 32 PF):
+  //   256x256x1  8 waves of 64x128, 1 workgroup per CU
+  //   128x128x1  4 waves of 64x64, 2
+  //   128x128x2  8 waves of 64x64, 1
+  //   64x64x2    8 waves of 16x64, 2
+  //   64x64x4    16 waves of 16x64, 1
   // A larger tile reads fewer bytes per product, a smaller one spreads a small
-  // problem over more of the 256 CUs and rounds M and N up less.  Measured
-  // microseconds per 128-deep K-group, for a tile alone on its CU, and per tile
-  // and CU when the CUs are full (int8, M = 128 .. 4096, K = 7168; FP8 has the
-  // same ratios):
-  //   256x256 1.24, 1.24    128x128 0.75, 0.49    64x128 0.62, 0.37    64x64 0.53, 0.31
+  // problem over more of the 256 CUs and rounds M and N up less; teams keep a CU
+  // busy that has one tile (more stages do not: a lone 64x64 tile took 35 us for
+  // 56 groups with 3 stages and with 6).  Measured microseconds per 128-deep
+  // K-group, for a CU's only tile, and per tile and CU when the CUs are full
+  // (int8, M = 80 .. 4096, K = 7168 and 18432; FP8 has the same ratios):
+  //   256x256x1 1.24  1.24    128x128x1 0.75  0.49    128x128x2 0.61  0.61
+  //   64x64x2   0.40  0.25    64x64x4   0.33  0.33
   // The problem's time per group is the first while every tile has a CU of its
-  // own, then the second per 256 tiles (whole rounds of 256x256), and the
-  // smallest wins: int8 512x7168x7168 70 / 42 / 38 / 60 us, 2048x7168x7168
-  // 80 / 96 / 146 / 206, 256x2048x7168 70 / 42 / 35 / 30.
-  const auto tiles = [&](int64_t bm, int64_t bn) {
+  // own, then the second per 256 tiles (in whole rounds where a CU holds one
+  // workgroup), and never less than the weight's 128 bytes a row take at the
+  // rate that each tiling was seen to stream a weight too large for the caches:
+  // 2.8, 3.3, 2.5, 2.5 and 2.8 TB/s.  The smallest wins.  Measured (us, in the
+  // order above):
+  //   int8  512x7168x7168   70  42  35  48  68
+  //   int8  128x7168x7168   68  43  35  23  19
+  //   int8 2048x7168x7168   80  96   -   -   -
+  //   int8 gated 64x18432x7168   -  67   -  80   -
+  //   int8 gated 128x18432x7168 94  81 107 107 126
+  //   FP8 gated 512x2048x7168   80  44  35  26  36
+  const int64_t kg = (p.K + 127) / 128;
+  const auto cost = [&](int64_t bm, int64_t bn, int64_t kw, float alone, float full, bool rounds, float tbs) {
     const int64_t cn = GATED ? bn / 2 : bn;
-    return float(((p.M + bm - 1) / bm) * ((p.N + cn - 1) / cn)) / 256.0f;
+    const float t = float(((p.M + bm - 1) / bm) * ((p.N + cn - 1) / cn)) / 256.0f;
+    float c = full * (rounds ? __builtin_ceilf(t) : t);
+    const float stream = float(p.N * (GATED ? 2 : 1)) * 128e-6f / tbs;
+    c = c > alone ? c : alone;
+    return (c > stream ? c : stream) * float((kg + kw - 1) / kw * kw);
   };
-  const auto most = [](float a, float b) { return a > b ? a : b; };
-  const float t256 = 1.24f * __builtin_ceilf(tiles(256, 256));
-  const float t128 = most(0.75f, 0.49f * tiles(128, 128));
-  const float t64x128 = most(0.62f, 0.37f * tiles(64, 128));
-  const float t64 = most(0.53f, 0.31f * tiles(64, 64));
-  if (t256 <= t128 && t256 <= t64x128 && t256 <= t64) return launch_tile_cfg<INT8, GATED, OUT, 256, 256, 4, 4, 2>(p, st);
-  if (t128 <= t64x128 && t128 <= t64) return launch_tile_cfg<INT8, GATED, OUT, 128, 128, 2, 2, 2>(p, st);
-  if (t64x128 <= t64) return launch_tile_cfg<INT8, GATED, OUT, 64, 128, 2, 2, 3>(p, st);
-  return launch_tile_cfg<INT8, GATED, OUT, 64, 64, 4, 2, 4>(p, st);
+  const float c[5] = {cost(256, 256, 1, 1.24f, 1.24f, true, 2.8f), cost(128, 128, 1, 0.75f, 0.49f, false, 3.3f),
+                      cost(128, 128, 2, 0.61f, 0.61f, true, 2.5f), cost(64, 64, 2, 0.40f, 0.25f, false, 2.5f),
+                      cost(64, 64, 4, 0.33f, 0.33f, true, 2.8f)};
+  int best = 0;
+  for (int i = 1; i < 5; ++i)
+    if (c[i] < c[best]) best = i;
+  switch (best) {
+    case 0: return launch_tile_cfg<INT8, GATED, OUT, 256, 256, 4, 4, 2, 1>(p, st);
+    case 1: return launch_tile_cfg<INT8, GATED, OUT, 128, 128, 2, 2, 2, 1>(p, st);
+    case 2: return launch_tile_cfg<INT8, GATED, OUT, 128, 128, 2, 2, 2, 2>(p, st);
+    case 3: return launch_tile_cfg<INT8, GATED, OUT, 64, 64, 4, 2, 2, 2>(p, st);
+    default: return launch_tile_cfg<INT8, GATED, OUT, 64, 64, 4, 2, 2, 4>(p, st);
+  }
 }
 
 }  // namespace fp8q

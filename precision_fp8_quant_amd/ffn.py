@@ -16,7 +16,7 @@ import ctypes
 
 import torch
 
-from . import (MAXABS, _cdiv, _codes, _dtype_code, _expect, _i64, _int, _ptr, _rowmajor, _run, lib)
+from . import BF16, F32, MAXABS, _cdiv, _codes, _dtype_code, _expect, _i64, _int, _ptr, _rowmajor, _run, lib
 
 # enum of include/fp8q_ffn.h
 ACT_SILU, ACT_GELU_TANH = 0, 1
@@ -46,31 +46,37 @@ def _ld(t):
     return max(cols + -cols % per, per)
 
 
-def _empty_rows16(rows, cols, dtype, device):
-    """A [rows][cols] tensor whose rows start at multiples of 16 bytes."""
-    pad = -cols % (16 // dtype.itemsize)
-    t = torch.empty((rows, cols + pad), dtype=dtype, device=device)
-    return t[:, :cols] if pad else t
+_OUT_CODE = {torch.bfloat16: BF16, torch.float32: F32}
 
 
-def _out(t, name, dtype, shape, device):
-    """The caller's output tensor, checked, or a new one."""
+def _out(t, name, dtype, rows, cols, device):
+    """The caller's output tensor, checked, or a new one; its dtype code and leading dimension."""
     if t is not None:
         dtype = t.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+    code = _OUT_CODE.get(dtype)
+    if code is None:
         raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
-    return _empty_rows16(*shape, dtype, device) if t is None else _expect(t, name, dtype, shape, device)
+    if t is None:
+        pad = -cols % (16 // dtype.itemsize)
+        t = torch.empty((rows, cols + pad), dtype=dtype, device=device)
+        return (t[:, :cols] if pad else t), code, max(cols + pad, 1)
+    _expect(t, name, dtype, (rows, cols), device)
+    return t, code, _ld(t)
 
 
 def _ints(t, name):
     """Leading dimension of an 8-bit integer operand, whose rows the library reads in whole 16-byte chunks."""
+    if t.dtype is torch.int8 and t.dim() == 2 and t.is_cuda:
+        rows, cols = t.shape
+        if cols % 16 == 0 and cols and t.stride(1) == 1:       # no chunk reaches beyond a row
+            return t.stride(0) if rows > 1 else cols
     _rowmajor(t, name)
     if t.dtype != torch.int8:
         raise TypeError(f"{name} must be torch.int8, got {t.dtype}")
     rows, cols = t.shape
     ld = _ld(t)
     # any other leading dimension is the ABI's FP8Q_ERR_ALIGN
-    if cols % 16 and rows and ld % 16 == 0:
+    if rows and cols and ld % 16 == 0:
         if t.storage_offset() + (rows - 1) * ld + cols + -cols % 16 > t.untyped_storage().nbytes():
             raise ValueError(f"{name}'s rows are read in whole 16-byte chunks: the storage must hold the last row up to "
                              "the next multiple of 16 bytes")
@@ -92,14 +98,15 @@ def fp8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bfloa
     _expect(b, "b", torch.uint8, (n2, k), dev)
     _expect(a_scales, "a_scales", torch.float32, (_cdiv(k, 128), m), dev, dense=True)
     _expect(b_scales, "b_scales", torch.float32, (_cdiv(n2, 128), _cdiv(k, 128)), dev, dense=True)
-    h = _out(h, "h", out_dtype, (m, f), dev)
+    h, code, ldh = _out(h, "h", out_dtype, m, f, dev)
+    gu_ptr, ldgu = None, 0
     if gu is not None or save_gate_up:
-        gu = _out(gu, "gu", h.dtype, (m, n2), dev)
-        if gu.dtype != h.dtype:
+        gu, gu_code, ldgu = _out(gu, "gu", h.dtype, m, n2, dev)
+        if gu_code != code:
             raise TypeError(f"gu must be {h.dtype} like h, got {gu.dtype}")
+        gu_ptr = gu.data_ptr()
     _run(lib.fp8_gemm_gated, dev, stream, act, m, f, k, a.data_ptr(), _ld(a), a_scales.data_ptr(), b.data_ptr(),
-         _ld(b), b_scales.data_ptr(), h.data_ptr(), _dtype_code(h), _ld(h), None if gu is None else gu.data_ptr(),
-         0 if gu is None else _ld(gu))
+         _ld(b), b_scales.data_ptr(), h.data_ptr(), code, ldh, gu_ptr, ldgu)
     return h if gu is None else (h, gu)
 
 
@@ -113,18 +120,23 @@ def fp8_gated_backward(dh, gu, act=ACT_SILU, mode=MAXABS, q=None, scales=None, q
     m, f = dh.shape
     dev, mp, f2 = dh.device, _cdiv(dh.shape[0], 128) * 128, 2 * dh.shape[1]
     _expect(gu, "gu", dh.dtype, (m, f2), dev)
+    ds, ts = (f2 // 128, mp), (mp // 128, f2)      # F is a multiple of 128 or the ABI's FP8Q_ERR_UNSUPPORTED
     if q is None:
         q = torch.empty((mp, f2), dtype=torch.uint8, device=dev)
+    else:
+        q = _expect(_codes(q), "q", torch.uint8, (mp, f2), dev)
     if scales is None:
-        scales = torch.empty((_cdiv(f2, 128), mp), dtype=torch.float32, device=dev)
+        scales = torch.empty(ds, dtype=torch.float32, device=dev)
+    else:
+        _expect(scales, "scales", torch.float32, ds, dev, dense=True)
     if q_t is None:
         q_t = torch.empty((f2, mp), dtype=torch.uint8, device=dev)
+    else:
+        q_t = _expect(_codes(q_t), "q_t", torch.uint8, (f2, mp), dev)
     if scales_t is None:
-        scales_t = torch.empty((_cdiv(mp, 128), f2), dtype=torch.float32, device=dev)
-    q = _expect(_codes(q), "q", torch.uint8, (mp, f2), dev)
-    _expect(scales, "scales", torch.float32, (_cdiv(f2, 128), mp), dev, dense=True)
-    q_t = _expect(_codes(q_t), "q_t", torch.uint8, (f2, mp), dev)
-    _expect(scales_t, "scales_t", torch.float32, (_cdiv(mp, 128), f2), dev, dense=True)
+        scales_t = torch.empty(ts, dtype=torch.float32, device=dev)
+    else:
+        _expect(scales_t, "scales_t", torch.float32, ts, dev, dense=True)
     if dgu is not None:
         _expect(dgu, "dgu", dh.dtype, (m, f2), dev)
     _run(lib.fp8_gated_backward, dev, stream, act, m, f, dh.data_ptr(), _ld(dh), gu.data_ptr(), _ld(gu),
@@ -140,12 +152,18 @@ def int8_quant_rows(x, q=None, scales=None, stream=None):
     rows, cols = x.shape
     dev = x.device
     if q is None:
-        q = _empty_rows16(rows, cols, torch.int8, dev)
+        ld = max(cols + -cols % 16, 16)
+        q = torch.empty((rows, ld), dtype=torch.int8, device=dev)
+        if ld != cols:
+            q = q[:, :cols]
+    else:
+        _expect(q, "q", torch.int8, (rows, cols), dev)
+        ld = _ld(q)
     if scales is None:
         scales = torch.empty((rows,), dtype=torch.float32, device=dev)
-    _expect(q, "q", torch.int8, (rows, cols), dev)
-    _expect(scales, "scales", torch.float32, (rows,), dev, dense=True)
-    _run(lib.int8_quant_rows, dev, stream, x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), q.data_ptr(), _ld(q),
+    else:
+        _expect(scales, "scales", torch.float32, (rows,), dev, dense=True)
+    _run(lib.int8_quant_rows, dev, stream, x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), q.data_ptr(), ld,
          scales.data_ptr())
     return q, scales
 
@@ -161,9 +179,9 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, out_dtype=torch.bfloat16, c=N
     _expect(b_scales, "b_scales", torch.float32, (n,), dev, dense=True)
     if bias is not None:
         _expect(bias, "bias", torch.float32, (n,), dev, dense=True)
-    c = _out(c, "c", out_dtype, (m, n), dev)
+    c, code, ldc = _out(c, "c", out_dtype, m, n, dev)
     _run(lib.int8_gemm, dev, stream, m, n, k, a.data_ptr(), lda, a_scales.data_ptr(), b.data_ptr(), ldb,
-         b_scales.data_ptr(), None if bias is None else bias.data_ptr(), c.data_ptr(), _dtype_code(c), _ld(c))
+         b_scales.data_ptr(), None if bias is None else bias.data_ptr(), c.data_ptr(), code, ldc)
     return c
 
 
@@ -179,7 +197,7 @@ def int8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bflo
     _expect(b, "b", torch.int8, (n2, k), dev)
     _expect(a_scales, "a_scales", torch.float32, (m,), dev, dense=True)
     _expect(b_scales, "b_scales", torch.float32, (n2,), dev, dense=True)
-    h = _out(h, "h", out_dtype, (m, n2 // 2), dev)
+    h, code, ldh = _out(h, "h", out_dtype, m, n2 // 2, dev)
     _run(lib.int8_gemm_gated, dev, stream, act, m, n2 // 2, k, a.data_ptr(), lda, a_scales.data_ptr(),
-         b.data_ptr(), ldb, b_scales.data_ptr(), h.data_ptr(), _dtype_code(h), _ld(h))
+         b.data_ptr(), ldb, b_scales.data_ptr(), h.data_ptr(), code, ldh)
     return h

@@ -266,6 +266,69 @@ def test_fp8_gemm_gated_bf16(m, f, k):
     assert og.rel_frobenius(_f64(gu), og.round_bf16(ref)) <= 1e-3
 
 
+# Rows and columns for which each of the kernels' tilings and streaming variants is the one chosen: 256x256, 128x128 by
+# one and by two teams, 64x64 by two and by four; one, two and four row fragments, 16 waves, two column fragments.
+VARIANTS = [(2000, 5300), (1300, 5000), (500, 7000), (500, 3000), (200, 1000), (3, 5000), (9, 6200), (30, 6200),
+            (40, 6200), (30, 3000), (20, 8000), (60, 8000), (40, 3000)]
+
+
+@pytest.mark.parametrize("m, n", VARIANTS)
+@pytest.mark.parametrize("k", [1101, 128])
+@pytest.mark.parametrize("gated", [False, True])
+def test_int8_every_variant(m, n, k, gated):
+    """Against the same product in 64 bits on the GPU (integers there are exact)."""
+    fp8q = require_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(m + n + k)
+    rnd = lambda r, c: torch.randint(-128, 128, (r, _up(c, 16)), generator=gen, device="cuda", dtype=torch.int8)  # noqa: E731
+    f = n // 2
+    rows = 2 * f if gated else n
+    a, b = rnd(m, k)[:, :k], rnd(rows, k)[:, :k]
+    sa = torch.rand(m, generator=gen, device="cuda") * (4.0 / (5000 * k ** 0.5)) + 1e-7
+    sb = torch.rand(rows, generator=gen, device="cuda") + 0.5
+    y = (a.double() @ b.double().t()) * sa.double()[:, None] * sb.double()[None, :]
+    if gated:
+        c, intact = _guarded(m, f, BF)
+        fp8q.int8_gemm_gated(a, sa, b, sb, act=of.GELU_TANH, h=c)
+        gu = _f64(y)
+        g, u = gu[:, :f], gu[:, f:]
+        ref = of.gated(g, u, of.GELU_TANH)
+        _near(c, ref, (22 + 20 * np.abs(_t(g, of.GELU_TANH))) * U * np.abs(ref) + TINY * (1 + np.abs(g * u)), BF)
+    else:
+        bias = torch.randn(n, generator=gen, device="cuda")
+        c, intact = _guarded(m, n, F32)
+        fp8q.int8_gemm(a, sa, b, sb, bias=bias, c=c)
+        ref = _f64(y + bias.double()[None, :])
+        _near(c, ref, 4 * U * (np.abs(_f64(y)) + np.abs(ref)) + TINY, F32)
+    intact()
+
+
+@pytest.mark.parametrize("m, f", [(2000, 2688), (1300, 2560), (500, 3584), (500, 1536), (200, 512), (3, 2560), (30, 3200),
+                                  (60, 4096), (20, 12160), (60, 2944)])
+@pytest.mark.parametrize("k", [1152, 128])
+def test_fp8_gated_every_variant(m, f, k):
+    """Gate and up against the product of the dequantized codes in 64 bits on the GPU, and h against them."""
+    fp8q = require_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(m + f + k)
+    x = torch.randn((m, k), generator=gen, device="cuda")
+    w = torch.randn((2 * f, k), generator=gen, device="cuda") * (1.5 / k ** 0.5)
+    qa, sa = fp8q.fp8_quant_tile(x, fp8q.TILE_1x128, fp8q.MAXABS)
+    qb, sb = fp8q.fp8_quant_block(w, fp8q.MAXABS)
+    h, h_intact = _guarded(m, f, F32)
+    gu, gu_intact = _guarded(m, 2 * f, F32)
+    fp8q.fp8_gemm_gated(qa, sa, qb, sb, h=h, gu=gu)
+    a = qa.view(torch.float8_e4m3fn).double() * sa.double().t().repeat_interleave(128, 1)
+    b = qb.view(torch.float8_e4m3fn).double() * sb.double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+    ref = a @ b.t()
+    rows = ((gu.double() - ref).norm(dim=1) / ref.norm(dim=1)).max().item()
+    cols = ((gu.double() - ref).norm(dim=0) / ref.norm(dim=0)).max().item()
+    assert rows <= 2e-4 and (m < 100 or cols <= 2e-4), (rows, cols)
+    g, u = _f64(gu)[:, :f], _f64(gu)[:, f:]
+    want = of.gated(g, u, of.SILU)
+    _near(h, want, (18 + 8 * np.abs(g)) * U * np.abs(want) + TINY * (1 + np.abs(g * u)), F32)
+    h_intact()
+    gu_intact()
+
+
 def test_fp8_gemm_gated_saturated_gates():
     """Gates of thousands on both sides: sigma is exactly 0 or 1 there and nothing overflows to NaN."""
     fp8q = require_gpu()
