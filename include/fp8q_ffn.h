@@ -97,7 +97,7 @@ int fp8_gated_backward(int act, int64_t M, int64_t F,
  * int8_quant_rows -- symmetric 8-bit codes with one scale for each row: a token
  * of an activation, an output channel of a weight stored [out][in].
  *   a = max(max_k |x[r][k]|, 127 * 2^-126)
- *   s = fl32(a / 127), inv = fl32(127 / a)  (IEEE divisions)
+ *   s = fl32(a * fl32(1/127)), inv = fl32(127 * fl32(1/a))  (IEEE operations)
  *   q = round-to-nearest-even(fl32(x * inv)), within [-127, 127]
  * The stored scale is the dequantization multiplier: x ~= s * q.
  *

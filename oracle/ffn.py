@@ -3,7 +3,7 @@
 Definitions (include/fp8q_ffn.h):
     * activations: SiLU g / (1 + e^-g), and GELU by its tanh form 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)));
     * gated product h = act(g) * u, and its gradient dg = dh * u * act'(g), du = dh * act(g);
-    * 8-bit codes of a row: a = max(max|x|, 127 * 2^-126), s = fl32(a / 127), inv = fl32(127 / a),
+    * 8-bit codes of a row: a = max(max|x|, 127 * 2^-126), s = fl32(a * fl32(1/127)), inv = fl32(127 * fl32(1/a)),
       q = round-half-even(fl32(x * inv));
     * integer product: a_scales[m] * b_scales[n] * sum_k A[m][k] B[n][k] (+ bias[n]).
 """
@@ -60,8 +60,9 @@ def quant_int8_rows(x):
     x = np.asarray(x, np.float32)
     amax = np.abs(x).max(axis=1) if x.shape[1] else np.zeros(x.shape[0], np.float32)
     a = np.maximum(amax, INT8_FLOOR).astype(np.float32)
-    s = (a / np.float32(127.0)).astype(np.float32)
-    inv = (np.float32(127.0) / a).astype(np.float32)
+    one = np.float32(1.0)
+    s = (a * (one / np.float32(127.0))).astype(np.float32)
+    inv = ((one / a).astype(np.float32) * np.float32(127.0)).astype(np.float32)
     q = np.rint((x * inv[:, None]).astype(np.float32))      # rint: half to even
     return q.astype(np.int8), s
 

@@ -1,8 +1,11 @@
 // 8-bit integer codes with one scale for each row.
 //
-//   a = max(max_k |x[r][k]|, 127 * 2^-126), s = fl32(a / 127), inv = fl32(127 / a)
+//   a = max(max_k |x[r][k]|, 127 * 2^-126)
+//   s = fl32(a * fl32(1/127)), inv = fl32(127 * fl32(1/a))
 //   q = rne(fl32(x * inv))
-// |x| <= a and inv <= (127 / a)(1 + 2^-24) keep |x inv| below 127.5, so the
+// (products with reciprocals rather than quotients: what a caller who writes the
+// rule with tensors gets, so that codes agree to the last one.)
+// |x| <= a and inv < (127 / a)(1 + 2^-20) keep |x inv| below 127.5, so the
 // rounded code needs no clamp.
 //
 // A streaming pass: a row is read once, held in registers between its maximum
@@ -103,8 +106,8 @@ __global__ __launch_bounds__(256) void int8_quant_rows_kernel(const T* __restric
 #pragma unroll
       for (int i = 0; i < R; ++i) m = run_max(m, v[i]);
       const float a = row_max<TPR>(m, wave_max);
-      const float inv = 127.0f / a;
-      if (t == 0) scales[r] = a / 127.0f;
+      const float inv = (1.0f / a) * 127.0f;
+      if (t == 0) scales[r] = a * (1.0f / 127.0f);
 #pragma unroll
       for (int i = 0; i < R; ++i) store_run(dst, int64_t(i * TPR + t) * 8, cols, v[i], inv);
     } else {
@@ -115,8 +118,8 @@ __global__ __launch_bounds__(256) void int8_quant_rows_kernel(const T* __restric
         m = run_max(m, v);
       }
       const float a = row_max<TPR>(m, wave_max);
-      const float inv = 127.0f / a;
-      if (t == 0) scales[r] = a / 127.0f;
+      const float inv = (1.0f / a) * 127.0f;
+      if (t == 0) scales[r] = a * (1.0f / 127.0f);
       for (int64_t c = t * 8; c < cols; c += TPR * 8) {
         float v[8];
         load_run(src, c, cols, v);
