@@ -124,7 +124,8 @@ int int8_quant_rows(const void* x, int x_dtype, int64_t rows, int64_t cols, int6
  * c        : C[M][N], leading dimension ldc, dtype c_dtype (FP8Q_BF16 or FP8Q_F32).
  * Any M, N and K from one token on.  Rows of A and B are read in whole
  * 16-byte chunks: the bytes from K up to the next multiple of 16 must be
- * readable in every row, the last one included; their values do not matter.
+ * readable in every row, the last one included, and the bytes between one row
+ * and the next may be read; their values do not matter.
  * Every code from -128 to 127 is allowed.  K of at most 131,056 (beyond it the
  * 32-bit sum could overflow) and lda, ldb of at most 4,194,176 bytes;
  * otherwise FP8Q_ERR_UNSUPPORTED.  M == 0 or N == 0 is a no-op; K == 0 writes

@@ -16,7 +16,7 @@ import ctypes
 
 import torch
 
-from . import BF16, F32, MAXABS, _cdiv, _codes, _dtype_code, _expect, _i64, _int, _ptr, _rowmajor, _run, lib
+from . import BF16, F32, MAXABS, OK, _cdiv, _check, _codes, _expect, _i64, _int, _ptr, _rowmajor, _run, lib
 
 # enum of include/fp8q_ffn.h
 ACT_SILU, ACT_GELU_TANH = 0, 1
@@ -37,46 +37,67 @@ for _name, _argtypes in SIGNATURES.items():
     getattr(lib, _name).restype = ctypes.c_int
 
 
+# A caller with few tokens waits for the host rather than for the kernel, so the checks below test the usual case in as
+# few expressions as they can and leave the message to the general ones.  Of a small int8_gemm call's 8 us the launch
+# is 3, the outputs' allocation 1.3 and the ctypes call 0.7.
+_bf16, _f32, _i8 = torch.bfloat16, torch.float32, torch.int8
+_CODE = {_bf16: BF16, _f32: F32}
+
+
+def _call(fn, dev, stream, *args):
+    if stream is None and torch._C._cuda_getDevice() == dev.index:      # the current device's current stream
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        if status != OK:
+            _check(status)
+    else:
+        _run(fn, dev, stream, *args)
+
+
 def _ld(t):
     """Leading dimension in elements; a single row's is its width in whole 16-byte chunks."""
     rows, cols = t.shape
     if rows > 1:
-        return t.stride(0)
+        return t.stride()[0]
     per = 16 // t.element_size()
     return max(cols + -cols % per, per)
 
 
-_OUT_CODE = {torch.bfloat16: BF16, torch.float32: F32}
+def _dense(t, name, shape, device):
+    """An FP32 array of scales or biases."""
+    if not (t.dtype is _f32 and t.shape == shape and t.is_contiguous() and t.device == device and t.is_cuda):
+        _expect(t, name, _f32, shape, device, dense=True)
+    return t.data_ptr()
 
 
 def _out(t, name, dtype, rows, cols, device):
     """The caller's output tensor, checked, or a new one; its dtype code and leading dimension."""
     if t is not None:
         dtype = t.dtype
-    code = _OUT_CODE.get(dtype)
+    code = _CODE.get(dtype)
     if code is None:
         raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
-    if t is None:
-        pad = -cols % (16 // dtype.itemsize)
-        t = torch.empty((rows, cols + pad), dtype=dtype, device=device)
-        return (t[:, :cols] if pad else t), code, max(cols + pad, 1)
-    _expect(t, name, dtype, (rows, cols), device)
-    return t, code, _ld(t)
+    if t is not None:
+        _expect(t, name, dtype, (rows, cols), device)
+        return t, code, _ld(t)
+    pad = -cols % (8 if code == BF16 else 4)
+    if pad:                                        # rows a multiple of 16 bytes apart
+        return torch.empty_strided((rows, cols), (cols + pad, 1), dtype=dtype, device=device), code, cols + pad
+    return torch.empty(rows, cols, dtype=dtype, device=device), code, cols or 1
 
 
 def _ints(t, name):
     """Leading dimension of an 8-bit integer operand, whose rows the library reads in whole 16-byte chunks."""
-    if t.dtype is torch.int8 and t.dim() == 2 and t.is_cuda:
-        rows, cols = t.shape
-        if cols % 16 == 0 and cols and t.stride(1) == 1:       # no chunk reaches beyond a row
-            return t.stride(0) if rows > 1 else cols
-    _rowmajor(t, name)
-    if t.dtype != torch.int8:
+    if not (t.dtype is _i8 and t.dim() == 2 and t.is_cuda):
+        _rowmajor(t, name)
         raise TypeError(f"{name} must be torch.int8, got {t.dtype}")
     rows, cols = t.shape
-    ld = _ld(t)
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        _rowmajor(t, name)
+    if rows <= 1:
+        ld = max(cols + -cols % 16, 16)
     # any other leading dimension is the ABI's FP8Q_ERR_ALIGN
-    if rows and cols and ld % 16 == 0:
+    if cols % 16 and rows and ld % 16 == 0:
         if t.storage_offset() + (rows - 1) * ld + cols + -cols % 16 > t.untyped_storage().nbytes():
             raise ValueError(f"{name}'s rows are read in whole 16-byte chunks: the storage must hold the last row up to "
                              "the next multiple of 16 bytes")
@@ -89,15 +110,16 @@ def fp8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bfloa
     gate and up weights in 128x128 blocks.  With save_gate_up=True (or a gu tensor) also gu[M][2F], the
     pre-activations that fp8_gated_backward takes."""
     a, b = _codes(_rowmajor(a, "a")), _codes(_rowmajor(b, "b"))
-    (m, k), (n2, dev) = a.shape, (b.shape[0], a.device)
-    if b.shape[1] != k:
+    (m, k), (n2, kb), dev = a.shape, b.shape, a.device
+    if kb != k:
         raise ValueError("a and b disagree on K")
     if n2 % 2:
         raise ValueError("b must hold as many gate rows as up rows")
-    f = n2 // 2
-    _expect(b, "b", torch.uint8, (n2, k), dev)
-    _expect(a_scales, "a_scales", torch.float32, (_cdiv(k, 128), m), dev, dense=True)
-    _expect(b_scales, "b_scales", torch.float32, (_cdiv(n2, 128), _cdiv(k, 128)), dev, dense=True)
+    if b.device != dev:
+        raise ValueError(f"b must be a tensor on {dev}")
+    f, kg = n2 // 2, _cdiv(k, 128)
+    sa = _dense(a_scales, "a_scales", (kg, m), dev)
+    sb = _dense(b_scales, "b_scales", (_cdiv(n2, 128), kg), dev)
     h, code, ldh = _out(h, "h", out_dtype, m, f, dev)
     gu_ptr, ldgu = None, 0
     if gu is not None or save_gate_up:
@@ -105,8 +127,8 @@ def fp8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bfloa
         if gu_code != code:
             raise TypeError(f"gu must be {h.dtype} like h, got {gu.dtype}")
         gu_ptr = gu.data_ptr()
-    _run(lib.fp8_gemm_gated, dev, stream, act, m, f, k, a.data_ptr(), _ld(a), a_scales.data_ptr(), b.data_ptr(),
-         _ld(b), b_scales.data_ptr(), h.data_ptr(), code, ldh, gu_ptr, ldgu)
+    _call(lib.fp8_gemm_gated, dev, stream, act, m, f, k, a.data_ptr(), _ld(a), sa, b.data_ptr(), _ld(b), sb,
+          h.data_ptr(), code, ldh, gu_ptr, ldgu)
     return h if gu is None else (h, gu)
 
 
@@ -117,31 +139,32 @@ def fp8_gated_backward(dh, gu, act=ACT_SILU, mode=MAXABS, q=None, scales=None, q
     scales_t [Mp/128][2F]: Wgrad's), Mp being M rounded up to whole 128-row tiles and the rows past M zero.  A dgu
     tensor [M][2F] also receives D itself."""
     _rowmajor(dh, "dh")
-    m, f = dh.shape
-    dev, mp, f2 = dh.device, _cdiv(dh.shape[0], 128) * 128, 2 * dh.shape[1]
-    _expect(gu, "gu", dh.dtype, (m, f2), dev)
+    (m, f), dev, dtype = dh.shape, dh.device, dh.dtype
+    code = _CODE.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (bfloat16 or float32)")
+    mp, f2 = m + -m % 128, 2 * f
+    _expect(gu, "gu", dtype, (m, f2), dev)
     ds, ts = (f2 // 128, mp), (mp // 128, f2)      # F is a multiple of 128 or the ABI's FP8Q_ERR_UNSUPPORTED
     if q is None:
-        q = torch.empty((mp, f2), dtype=torch.uint8, device=dev)
+        q = torch.empty(mp, f2, dtype=torch.uint8, device=dev)
     else:
         q = _expect(_codes(q), "q", torch.uint8, (mp, f2), dev)
     if scales is None:
-        scales = torch.empty(ds, dtype=torch.float32, device=dev)
-    else:
-        _expect(scales, "scales", torch.float32, ds, dev, dense=True)
+        scales = torch.empty(*ds, dtype=_f32, device=dev)
     if q_t is None:
-        q_t = torch.empty((f2, mp), dtype=torch.uint8, device=dev)
+        q_t = torch.empty(f2, mp, dtype=torch.uint8, device=dev)
     else:
         q_t = _expect(_codes(q_t), "q_t", torch.uint8, (f2, mp), dev)
     if scales_t is None:
-        scales_t = torch.empty(ts, dtype=torch.float32, device=dev)
-    else:
-        _expect(scales_t, "scales_t", torch.float32, ts, dev, dense=True)
+        scales_t = torch.empty(*ts, dtype=_f32, device=dev)
+    s, st = _dense(scales, "scales", ds, dev), _dense(scales_t, "scales_t", ts, dev)
+    dgu_ptr, ld_dgu = None, 0
     if dgu is not None:
-        _expect(dgu, "dgu", dh.dtype, (m, f2), dev)
-    _run(lib.fp8_gated_backward, dev, stream, act, m, f, dh.data_ptr(), _ld(dh), gu.data_ptr(), _ld(gu),
-         _dtype_code(dh), mode, q.data_ptr(), _ld(q), scales.data_ptr(), q_t.data_ptr(), _ld(q_t),
-         scales_t.data_ptr(), None if dgu is None else dgu.data_ptr(), 0 if dgu is None else _ld(dgu))
+        _expect(dgu, "dgu", dtype, (m, f2), dev)
+        dgu_ptr, ld_dgu = dgu.data_ptr(), _ld(dgu)
+    _call(lib.fp8_gated_backward, dev, stream, act, m, f, dh.data_ptr(), _ld(dh), gu.data_ptr(), _ld(gu), code, mode,
+          q.data_ptr(), _ld(q), s, q_t.data_ptr(), _ld(q_t), st, dgu_ptr, ld_dgu)
     return q, scales, q_t, scales_t
 
 
@@ -149,39 +172,38 @@ def int8_quant_rows(x, q=None, scales=None, stream=None):
     """Symmetric 8-bit codes of a 2-D bf16/fp32 tensor with one scale for each row (token or output channel):
     q int8 [rows][cols], scales [rows], x ~= q * scales[:, None]."""
     _rowmajor(x, "x")
-    rows, cols = x.shape
-    dev = x.device
+    (rows, cols), dev = x.shape, x.device
+    code = _CODE.get(x.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {x.dtype} (bfloat16 or float32)")
     if q is None:
-        ld = max(cols + -cols % 16, 16)
-        q = torch.empty((rows, ld), dtype=torch.int8, device=dev)
+        ld = max(cols + -cols % 16, 16)            # the last row's bytes up to 16 exist too, as int8_gemm reads them
+        q = torch.empty(rows, ld, dtype=_i8, device=dev)
         if ld != cols:
-            q = q[:, :cols]
+            q = q.as_strided((rows, cols), (ld, 1))
     else:
-        _expect(q, "q", torch.int8, (rows, cols), dev)
+        _expect(q, "q", _i8, (rows, cols), dev)
         ld = _ld(q)
     if scales is None:
-        scales = torch.empty((rows,), dtype=torch.float32, device=dev)
-    else:
-        _expect(scales, "scales", torch.float32, (rows,), dev, dense=True)
-    _run(lib.int8_quant_rows, dev, stream, x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), q.data_ptr(), ld,
-         scales.data_ptr())
+        scales = torch.empty(rows, dtype=_f32, device=dev)
+    _call(lib.int8_quant_rows, dev, stream, x.data_ptr(), code, rows, cols, _ld(x), q.data_ptr(), ld,
+          _dense(scales, "scales", (rows,), dev))
     return q, scales
 
 
 def int8_gemm(a, a_scales, b, b_scales, bias=None, out_dtype=torch.bfloat16, c=None, stream=None):
     """C[M][N] = a_scales[m] * b_scales[n] * (A . B^T) (+ bias[n]) from 8-bit integers a [M][K] and b [N][K]."""
     lda, ldb = _ints(a, "a"), _ints(b, "b")
-    (m, k), n, dev = a.shape, b.shape[0], a.device
-    if b.shape[1] != k:
+    (m, k), (n, kb), dev = a.shape, b.shape, a.device
+    if kb != k:
         raise ValueError("a and b disagree on K")
-    _expect(b, "b", torch.int8, (n, k), dev)
-    _expect(a_scales, "a_scales", torch.float32, (m,), dev, dense=True)
-    _expect(b_scales, "b_scales", torch.float32, (n,), dev, dense=True)
-    if bias is not None:
-        _expect(bias, "bias", torch.float32, (n,), dev, dense=True)
+    if b.device != dev:
+        raise ValueError(f"b must be a tensor on {dev}")
+    sa, sb = _dense(a_scales, "a_scales", (m,), dev), _dense(b_scales, "b_scales", (n,), dev)
+    bias_ptr = None if bias is None else _dense(bias, "bias", (n,), dev)
     c, code, ldc = _out(c, "c", out_dtype, m, n, dev)
-    _run(lib.int8_gemm, dev, stream, m, n, k, a.data_ptr(), lda, a_scales.data_ptr(), b.data_ptr(), ldb,
-         b_scales.data_ptr(), None if bias is None else bias.data_ptr(), c.data_ptr(), code, ldc)
+    _call(lib.int8_gemm, dev, stream, m, n, k, a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, bias_ptr, c.data_ptr(),
+          code, ldc)
     return c
 
 
@@ -189,15 +211,15 @@ def int8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bflo
     """h[M][F] = act(g) * u with g and u the int8_gemm products of a [M][K] and the stacked gate and up weights
     b [2F][K]."""
     lda, ldb = _ints(a, "a"), _ints(b, "b")
-    (m, k), n2, dev = a.shape, b.shape[0], a.device
-    if b.shape[1] != k:
+    (m, k), (n2, kb), dev = a.shape, b.shape, a.device
+    if kb != k:
         raise ValueError("a and b disagree on K")
     if n2 % 2:
         raise ValueError("b must hold as many gate rows as up rows")
-    _expect(b, "b", torch.int8, (n2, k), dev)
-    _expect(a_scales, "a_scales", torch.float32, (m,), dev, dense=True)
-    _expect(b_scales, "b_scales", torch.float32, (n2,), dev, dense=True)
+    if b.device != dev:
+        raise ValueError(f"b must be a tensor on {dev}")
+    sa, sb = _dense(a_scales, "a_scales", (m,), dev), _dense(b_scales, "b_scales", (n2,), dev)
     h, code, ldh = _out(h, "h", out_dtype, m, n2 // 2, dev)
-    _run(lib.int8_gemm_gated, dev, stream, act, m, n2 // 2, k, a.data_ptr(), lda, a_scales.data_ptr(),
-         b.data_ptr(), ldb, b_scales.data_ptr(), h.data_ptr(), code, ldh)
+    _call(lib.int8_gemm_gated, dev, stream, act, m, n2 // 2, k, a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb,
+          h.data_ptr(), code, ldh)
     return h
