@@ -16,6 +16,7 @@ struct FfnArgs {
   void* c; int64_t ldc;           // C[M][N], or h[M][F]
   void* gu; int64_t ldgu;         // gate and up before the activation, or nullptr
   int64_t M, N, K;                // N: columns of c (F where the product is gated)
+  int64_t up;                     // gated: rows of b (scales, columns of gu) from the gate's to the up's
   float act_c1, act_c3;           // the activation's sigma argument (gate_act.h)
 };
 

@@ -2,7 +2,7 @@
 // memory straight into matrix-instruction registers.
 //
 //   plain:  C[m][n] = sa[m] sb[n] sum_k A[m][k] B[n][k] (+ bias[n])
-//   gated:  h[m][f] = act(g) u,  g from B's rows [0, N), u from rows [N, 2N)
+//   gated:  h[m][f] = act(g) u,  g from B's rows [0, N), u from rows [up, up + N)
 // with 8-bit integers (32-bit integer sums, scales per row of A and B) or
 // block-scaled FP8 (one FP32 promotion per 128-deep K-group with that group's
 // scales, as in gemm_kernel.h).
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
     const int64_t c = n0 + 16 * f + lr;
     const int64_t n = c < p.N ? c : p.N - 1;
 #pragma unroll
-    for (int b = 0; b < NP; ++b) brow[b][f] = p.b + (b * p.N + n) * p.ldb + 16 * lq;
+    for (int b = 0; b < NP; ++b) brow[b][f] = p.b + (b * p.up + n) * p.ldb + 16 * lq;
   }
 
   acc_t acc[NP][NF][MF];
@@ -132,7 +132,7 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
 #pragma unroll
       for (int i = 0; i < MF; ++i) x.sa[i] = p.sa[g * p.M + mrow[i]];
 #pragma unroll
-      for (int b = 0; b < NP; ++b) x.sb[b] = p.sb[((b * p.N + n0) >> 7) * KG + g];
+      for (int b = 0; b < NP; ++b) x.sb[b] = p.sb[((b * p.up + n0) >> 7) * KG + g];
     }
   };
   auto use = [&](const Group& x) {
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
     if (p.K > 0 && tid < 16 * MF) my_sa = p.sa[m0 + tid < p.M ? m0 + tid : p.M - 1];
     if (tid < NP * NF * 16) {
       const int64_t c = n0 + tid % (NF * 16), n = c < p.N ? c : p.N - 1;
-      if (p.K > 0) my_sb = p.sb[tid / (NF * 16) * p.N + n];
+      if (p.K > 0) my_sb = p.sb[tid / (NF * 16) * p.up + n];
       if (!GATED && p.bias) my_bias = p.bias[n];
     }
   }
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
       if constexpr (GATED)
         if (p.gu) {
           store(p.gu, p.ldgu, n, y[0]);
-          store(p.gu, p.ldgu, p.N + n, y[1]);
+          store(p.gu, p.ldgu, p.up + n, y[1]);
         }
     }
   }

@@ -2,7 +2,7 @@
 // as stream_kernel.h.
 //
 //   plain:  C[m][n] = sa[m] sb[n] sum_k A[m][k] B[n][k] (+ bias[n])
-//   gated:  h[m][f] = act(g) u,  g from B's rows [0, N), u from rows [N, 2N)
+//   gated:  h[m][f] = act(g) u,  g from B's rows [0, N), u from rows [up, up + N)
 //
 // The data path is the one of gemm_kernel.h: per 128-deep K-group, global ->
 // LDS by LDS DMA (16-byte chunks XOR-swizzled by row, B rows in fragment
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
   const int kr = int((p.K + 15) & ~int64_t(15));
   const uint8_t* const a_base = p.a + m0 * p.lda;
   const uint8_t* const b_base = p.b + n0 * p.ldb;
-  const uint8_t* const u_base = p.b + ((GATED ? p.N : 0) + n0) * p.ldb;
+  const uint8_t* const u_base = p.b + ((GATED ? p.up : 0) + n0) * p.ldb;
   const int a_end = int((mrows - 1) * p.lda) + kr;
   const int b_end = int((nrows - 1) * p.ldb) + kr;
   int a_off[A_DMA], b_off[B_DMA];
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
         __builtin_amdgcn_global_load_lds((gptr_t)src, (lptr_t)(s + 256 * wave), 4, 0, 0);
       }
       if (wave == NW - 1 && lane < 2) {
-        const float* src = p.sb + (((lane ? p.N : 0) + n0) >> 7) * KG + g;
+        const float* src = p.sb + (((lane ? p.up : 0) + n0) >> 7) * KG + g;
         __builtin_amdgcn_global_load_lds((gptr_t)src, (lptr_t)(s + BM * 4), 4, 0, 0);
       }
     }
@@ -322,7 +322,7 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int64_t c = n_wave + (GATED ? 0 : PC * pn) + 4 * PF * lq + 4 * js + j;
-            const float sb = p.sb[(GATED && pn ? p.N : 0) + (c < p.N ? c : p.N - 1)];
+            const float sb = p.sb[(GATED && pn ? p.up : 0) + (c < p.N ? c : p.N - 1)];
 #pragma unroll
             for (int ms = 0; ms < SM; ++ms) y[ms][pn][js][j] *= sa[ms] * sb;
           }
@@ -364,6 +364,13 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
     }
     const int chunk = lane % LPR;
     const int64_t n = col0 + chunk * EPC;
+    // BF16 rows of whole 128-byte lines go past the caches (int8 8192x7168x18432
+    // 824 us, 832 kept in them); others leave partial lines that the L2 has to
+    // join first (2000x9300x1024 BF16 48.8 us past the caches, 33.0 through
+    // them; FP32 66.6 and 40.8), and FP32 gains from them anyhow (2048x8192x1024
+    // 27.2 and 25.3).
+    const bool past_cache =
+        ESZ == 2 && ((ld * ESZ | int64_t(reinterpret_cast<uintptr_t>(dst)) | col0 * ESZ) & 127) == 0;
 #pragma unroll
     for (int sr = 0; sr < (TM + RPI - 1) / RPI; ++sr) {
       const int r = sr * RPI + lane / LPR;
@@ -372,7 +379,8 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
       const u32x4 v = *reinterpret_cast<const u32x4*>(stg + r * PITCH + 16 * chunk);
       uint8_t* out = static_cast<uint8_t*>(dst) + (m * ld + n) * ESZ;
       if (n + EPC <= end) {
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out));
+        if (past_cache) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out));
+        else *reinterpret_cast<u32x4*>(out) = v;
       } else {
         for (int e = 0; e < int(end - n); ++e) {
           if constexpr (OUT == kOutBF16)
@@ -386,7 +394,7 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
   if constexpr (GATED) {
     if (p.gu) {
       emit(0, p.gu, p.ldgu, n_wave, p.N);
-      emit(1, p.gu, p.ldgu, p.N + n_wave, 2 * p.N);
+      emit(1, p.gu, p.ldgu, p.up + n_wave, p.up + p.N);
     }
 #pragma unroll
     for (int ms = 0; ms < SM; ++ms)
@@ -454,6 +462,26 @@ static hipError_t launch_tile(const FfnArgs& p, hipStream_t st) {
   int best = 0;
   for (int i = 1; i < 5; ++i)
     if (c[i] < c[best]) best = i;
+  if (best == 0) {
+    // A last round of 256x256 tiles that is at most half full, in whole bands of
+    // columns, runs as a problem of its own right behind the others, in smaller
+    // tiles (int8 8192x7168x18432, 3.5 rounds: 857 -> 820 us).
+    constexpr int64_t CN = GATED ? 128 : 256;
+    const int64_t tm = (p.M + 255) / 256, tn = (p.N + CN - 1) / CN, tail = tm * tn % 256;
+    if (tm * tn > 256 && tail != 0 && tail <= 128 && tail % tm == 0) {
+      const int64_t cut = (tn - tail / tm) * CN, es = OUT == kOutBF16 ? 2 : 4;
+      FfnArgs head = p, rest = p;
+      head.N = cut;
+      rest.N = p.N - cut;
+      rest.b = p.b + cut * p.ldb;
+      rest.sb = p.sb + (INT8 ? cut : cut / 128 * kg);
+      rest.bias = p.bias ? p.bias + cut : nullptr;
+      rest.c = static_cast<uint8_t*>(p.c) + cut * es;
+      rest.gu = p.gu ? static_cast<uint8_t*>(p.gu) + cut * es : nullptr;
+      const hipError_t e = launch_tile_cfg<INT8, GATED, OUT, 256, 256, 4, 4, 2, 1>(head, st);
+      return e != hipSuccess ? e : launch_tile<INT8, GATED, OUT>(rest, st);
+    }
+  }
   switch (best) {
     case 0: return launch_tile_cfg<INT8, GATED, OUT, 256, 256, 4, 4, 2, 1>(p, st);
     case 1: return launch_tile_cfg<INT8, GATED, OUT, 128, 128, 2, 2, 2, 1>(p, st);
