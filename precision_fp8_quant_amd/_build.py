@@ -1,4 +1,4 @@
-"""Compile the fp8q HIP library (libfp8q.so) in-tree for gfx950.
+"""Compile the fp8q HIP library (libfp8q.so) and its native call path (_ffn_call.so) in-tree for gfx950.
 
 Every kernel is hand-written HIP for CDNA4; this only drives hipcc.  The
 library is linked into ``precision_fp8_quant_amd/libfp8q.so`` next to the
@@ -35,6 +35,34 @@ PER_SOURCE_FLAGS = {"gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
                     "ffn/fp8_gated.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
+# The native call path of ffn.py: a CPython extension against torch's headers,
+# linked to libfp8q.so beside it.
+BINDING_SRC = os.path.join(CSRC, "ffn", "binding.cpp")
+BINDING_PATH = os.path.join(PKG_DIR, "_ffn_call.so")
+
+
+def _binding_command(out):
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(rocm, "include"), BINDING_SRC, "-o", out]
+
+
+def _link_binding(obj, verbose):
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_PATH + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, "-L", libs, "-ltorch", "-ltorch_cpu", "-ltorch_python",
+          "-lc10", "-lc10_hip", "-L", PKG_DIR, "-lfp8q", "-Wl,-rpath,$ORIGIN"], verbose)
+    os.replace(tmp, BINDING_PATH)
+
+
 def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -45,7 +73,7 @@ def _run(cmd, verbose):
 
 
 def build(verbose=False, extra_flags=()):
-    """Compile every source and link libfp8q.so (always recompiles)."""
+    """Compile every source and link libfp8q.so and the native call path (always recompiles)."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = []
     for src in DEVICE_SOURCES:
@@ -55,12 +83,14 @@ def build(verbose=False, extra_flags=()):
     for src in HOST_SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace("/", "_") + ".o")
         jobs.append([HIPCC, *COMMON_FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj])
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-        list(ex.map(lambda c: _run(c, verbose), jobs))
     objs = [j[-1] for j in jobs]
+    binding = os.path.join(BUILD_DIR, "ffn_binding.cpp.o")
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        list(ex.map(lambda c: _run(c, verbose), [*jobs, _binding_command(binding)]))
     tmp = LIB_PATH + ".tmp"
     _run([HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding, verbose)
     return LIB_PATH
 
 

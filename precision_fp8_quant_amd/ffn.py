@@ -17,6 +17,7 @@ import ctypes
 import torch
 
 from . import BF16, F32, MAXABS, OK, _cdiv, _check, _codes, _expect, _i64, _int, _ptr, _rowmajor, _run, lib
+from . import _ffn_call as _native
 
 # enum of include/fp8q_ffn.h
 ACT_SILU, ACT_GELU_TANH = 0, 1
@@ -37,11 +38,18 @@ for _name, _argtypes in SIGNATURES.items():
     getattr(lib, _name).restype = ctypes.c_int
 
 
-# A caller with few tokens waits for the host rather than for the kernel, so the checks below test the usual case in as
-# few expressions as they can and leave the message to the general ones.  Of a small int8_gemm call's 8 us the launch
-# is 3, the outputs' allocation 1.3 and the ctypes call 0.7.
+# A caller with few tokens waits for the host rather than for the kernel.  The usual call (new outputs, current device
+# and stream) is made by csrc/ffn/binding.cpp in one step; it answers None for anything else, and an int where the C ABI
+# refuses.  What follows it here takes every call, and says what is wrong with one.
 _bf16, _f32, _i8 = torch.bfloat16, torch.float32, torch.int8
 _CODE = {_bf16: BF16, _f32: F32}
+
+
+def _done(r):
+    """The native call's answer: a result, or the C ABI's refusal as an error."""
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def _call(fn, dev, stream, *args):
@@ -109,6 +117,10 @@ def fp8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bfloa
     """h[M][F] = act(A Bg^T) * (A Bu^T) from block-scaled FP8 operands: a [M][K] in 1x128 tiles, b [2F][K] the stacked
     gate and up weights in 128x128 blocks.  With save_gate_up=True (or a gu tensor) also gu[M][2F], the
     pre-activations that fp8_gated_backward takes."""
+    if h is None and gu is None and stream is None:
+        r = _native.fp8_gemm_gated(a, a_scales, b, b_scales, act, _CODE.get(out_dtype), save_gate_up)
+        if r is not None:
+            return _done(r)
     a, b = _codes(_rowmajor(a, "a")), _codes(_rowmajor(b, "b"))
     (m, k), (n2, kb), dev = a.shape, b.shape, a.device
     if kb != k:
@@ -138,6 +150,10 @@ def fp8_gated_backward(dh, gu, act=ACT_SILU, mode=MAXABS, q=None, scales=None, q
     1x128 tiles (q [Mp][2F], scales [2F/128][Mp]: Dgrad's operand) and transposed 128x1 tiles (q_t [2F][Mp],
     scales_t [Mp/128][2F]: Wgrad's), Mp being M rounded up to whole 128-row tiles and the rows past M zero.  A dgu
     tensor [M][2F] also receives D itself."""
+    if q is None and scales is None and q_t is None and scales_t is None and dgu is None and stream is None:
+        r = _native.fp8_gated_backward(dh, gu, act, mode)
+        if r is not None:
+            return _done(r)
     _rowmajor(dh, "dh")
     (m, f), dev, dtype = dh.shape, dh.device, dh.dtype
     code = _CODE.get(dtype)
@@ -171,6 +187,10 @@ def fp8_gated_backward(dh, gu, act=ACT_SILU, mode=MAXABS, q=None, scales=None, q
 def int8_quant_rows(x, q=None, scales=None, stream=None):
     """Symmetric 8-bit codes of a 2-D bf16/fp32 tensor with one scale for each row (token or output channel):
     q int8 [rows][cols], scales [rows], x ~= q * scales[:, None]."""
+    if q is None and scales is None and stream is None:
+        r = _native.int8_quant_rows(x)
+        if r is not None:
+            return _done(r)
     _rowmajor(x, "x")
     (rows, cols), dev = x.shape, x.device
     code = _CODE.get(x.dtype)
@@ -193,6 +213,10 @@ def int8_quant_rows(x, q=None, scales=None, stream=None):
 
 def int8_gemm(a, a_scales, b, b_scales, bias=None, out_dtype=torch.bfloat16, c=None, stream=None):
     """C[M][N] = a_scales[m] * b_scales[n] * (A . B^T) (+ bias[n]) from 8-bit integers a [M][K] and b [N][K]."""
+    if c is None and stream is None:
+        r = _native.int8_gemm(a, a_scales, b, b_scales, bias, _CODE.get(out_dtype))
+        if r is not None:
+            return _done(r)
     lda, ldb = _ints(a, "a"), _ints(b, "b")
     (m, k), (n, kb), dev = a.shape, b.shape, a.device
     if kb != k:
@@ -210,6 +234,10 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, out_dtype=torch.bfloat16, c=N
 def int8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bfloat16, h=None, stream=None):
     """h[M][F] = act(g) * u with g and u the int8_gemm products of a [M][K] and the stacked gate and up weights
     b [2F][K]."""
+    if h is None and stream is None:
+        r = _native.int8_gemm_gated(a, a_scales, b, b_scales, act, _CODE.get(out_dtype))
+        if r is not None:
+            return _done(r)
     lda, ldb = _ints(a, "a"), _ints(b, "b")
     (m, k), (n2, kb), dev = a.shape, b.shape, a.device
     if kb != k:

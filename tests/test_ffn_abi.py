@@ -162,3 +162,18 @@ def test_int8_codes_of_a_worked_row():
     assert s[0] == 2.0 and q.tolist() == [[127, 0, 2, 2, 0, -2, -127, 0]]
     q, s = of.quant_int8_rows(np.zeros((1, 3), np.float32))
     assert s[0] == np.float32(2.0 ** -126) and not q.any()
+
+
+def test_native_call_leaves_unusual_calls_to_the_binding():
+    """What the native call path does not expect it leaves alone (None): ffn.py then names what is wrong."""
+    import torch
+    from precision_fp8_quant_amd import _ffn_call as native
+    i8, s = torch.zeros((4, 32), dtype=torch.int8), torch.ones(4)
+    assert native.int8_gemm(i8, s, i8, s, None, fp8q.BF16) is None                 # host tensors
+    assert native.int8_gemm(1, None, "a", s, 2.5, 1 << 80) is None
+    assert native.int8_gemm() is None and native.fp8_gated_backward(i8) is None
+    assert native.int8_gemm_gated(i8, s, i8, s, -1, fp8q.BF16) is None
+    assert native.fp8_gemm_gated(i8, s, i8, s, 0, 0, 1) is None
+    assert native.int8_quant_rows(s) is None
+    with pytest.raises(ValueError, match="must be a device tensor"):
+        fp8q.int8_gemm(i8, s, i8, s)
