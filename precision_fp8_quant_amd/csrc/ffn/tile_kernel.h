@@ -435,41 +435,54 @@ static hipError_t launch_tile(const FfnArgs& p, hipStream_t st) {
   // (int8, M = 80 .. 4096, K = 7168 and 18432; FP8 has the same ratios):
   //   256x256x1 1.24  1.24    128x128x1 0.75  0.49    128x128x2 0.61  0.61
   //   64x64x2   0.40  0.25    64x64x4   0.33  0.33
-  // The problem's time per group is the first while every tile has a CU of its
-  // own, then the second per 256 tiles (in whole rounds where a CU holds one
-  // workgroup), and never less than the weight's 128 bytes a row take at the
-  // rate that each tiling was seen to stream a weight too large for the caches:
-  // 2.8, 3.3, 2.5, 2.5 and 2.8 TB/s.  The smallest wins.  Measured (us, in the
-  // order above):
+  // A problem runs in rounds.  Where a CU holds one workgroup, each round of 256
+  // tiles, full or not, takes the one time per group.  Where it holds two, a
+  // round is 512 tiles and takes twice the second time; a last round takes the
+  // first time up to 256 tiles and a line between the two beyond.  The time is
+  // never less than the weight's 128 bytes a row take at the rate that each
+  // tiling was seen to stream a weight too large for the caches: 2.8, 3.3, 2.5,
+  // 2.5 and 2.8 TB/s.  The smallest wins.  Measured (us, in the order above):
   //   int8  512x7168x7168   70  42  35  48  68
   //   int8  128x7168x7168   68  43  35  23  19
   //   int8 2048x7168x7168   80  96   -   -   -
   //   int8 gated 64x18432x7168   -  67   -  80   -
   //   int8 gated 128x18432x7168 94  81 107 107 126
   //   FP8 gated 512x2048x7168   80  44  35  26  36
+  //   FP8 gated 1846x640x6016   70  38  32  41  47   (580 tiles of 64x64)
+  //   FP8 gated 4096x1408x2048  33  36  43  52  77
   const int64_t kg = (p.K + 127) / 128;
-  const auto cost = [&](int64_t bm, int64_t bn, int64_t kw, float alone, float full, bool rounds, float tbs) {
-    const int64_t cn = GATED ? bn / 2 : bn;
-    const float t = float(((p.M + bm - 1) / bm) * ((p.N + cn - 1) / cn)) / 256.0f;
-    float c = full * (rounds ? __builtin_ceilf(t) : t);
-    const float stream = float(p.N * (GATED ? 2 : 1)) * 128e-6f / tbs;
-    c = c > alone ? c : alone;
-    return (c > stream ? c : stream) * float((kg + kw - 1) / kw * kw);
+  const auto cost = [&](int64_t n, int i) {        // microseconds for n of the N columns in tiling i
+    struct Tiling { int64_t bm, bn, kw; float alone, full, tbs; };
+    constexpr Tiling tilings[5] = {{256, 256, 1, 1.24f, 1.24f, 2.8f}, {128, 128, 1, 0.75f, 0.49f, 3.3f},
+                                   {128, 128, 2, 0.61f, 0.61f, 2.5f}, {64, 64, 2, 0.40f, 0.25f, 2.5f},
+                                   {64, 64, 4, 0.33f, 0.33f, 2.8f}};
+    const Tiling& s = tilings[i];
+    const int64_t cn = GATED ? s.bn / 2 : s.bn;
+    const int64_t tiles = ((p.M + s.bm - 1) / s.bm) * ((n + cn - 1) / cn), two = s.alone != s.full ? 2 : 1;
+    const int64_t last = tiles % (256 * two);
+    const float beyond = last > 256 ? float(last - 256) / 256.0f : 0.0f;
+    float c = float(tiles / (256 * two) * two) * s.full;
+    c += last ? s.alone + beyond * (2 * s.full - s.alone) : 0.0f;
+    const float stream = float(n * (GATED ? 2 : 1)) * 128e-6f / s.tbs;
+    return (c > stream ? c : stream) * float((kg + s.kw - 1) / s.kw * s.kw);
   };
-  const float c[5] = {cost(256, 256, 1, 1.24f, 1.24f, true, 2.8f), cost(128, 128, 1, 0.75f, 0.49f, false, 3.3f),
-                      cost(128, 128, 2, 0.61f, 0.61f, true, 2.5f), cost(64, 64, 2, 0.40f, 0.25f, false, 2.5f),
-                      cost(64, 64, 4, 0.33f, 0.33f, true, 2.8f)};
-  int best = 0;
-  for (int i = 1; i < 5; ++i)
-    if (c[i] < c[best]) best = i;
-  if (best == 0) {
-    // A last round of 256x256 tiles that is at most half full, in whole bands of
-    // columns, runs as a problem of its own right behind the others, in smaller
-    // tiles (int8 8192x7168x18432, 3.5 rounds: 857 -> 820 us).
-    constexpr int64_t CN = GATED ? 128 : 256;
-    const int64_t tm = (p.M + 255) / 256, tn = (p.N + CN - 1) / CN, tail = tm * tn % 256;
-    if (tm * tn > 256 && tail != 0 && tail <= 128 && tail % tm == 0) {
-      const int64_t cut = (tn - tail / tm) * CN, es = OUT == kOutBF16 ? 2 : 4;
+  const auto pick = [&](int64_t n) {
+    int best = 0;
+    for (int i = 1; i < 5; ++i)
+      if (cost(n, i) < cost(n, best)) best = i;
+    return best;
+  };
+  const int best = pick(p.N);
+  // Whole columns of 256x256 tiles that fill rounds, and the other columns right
+  // behind them as a problem of their own in smaller tiles, where that is less
+  // by more than a launch (int8 8192x7168x18432, 3.5 rounds: 857 -> 820 us;
+  // int8 4200x4096x4096, 272 tiles: 85 -> 70; FP8 gated 2239x4608x3840: 100 -> 87).
+  constexpr int64_t CN = GATED ? 128 : 256;
+  const int64_t tm = (p.M + 255) / 256, tn = (p.N + CN - 1) / CN;
+  const int64_t whole = tm * tn / 256 * 256 / tm;  // such columns
+  if (whole > 0 && whole < tn) {
+    const int64_t cut = whole * CN, es = OUT == kOutBF16 ? 2 : 4;
+    if (cost(cut, 0) + cost(p.N - cut, pick(p.N - cut)) + 3.0f < cost(p.N, best)) {
       FfnArgs head = p, rest = p;
       head.N = cut;
       rest.N = p.N - cut;

@@ -330,6 +330,17 @@ def test_fp8_gated_every_variant(m, f, k):
     gu_intact()
 
 
+@pytest.mark.parametrize("m, n", [(4200, 4059), (3300, 5700)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_int8_round_and_a_few_tiles(m, n, gated):
+    """A few 256x256 tiles more than one for each CU, the last ones not a whole number of columns."""
+    test_int8_every_variant(m, n, 1101, gated)
+
+
+def test_fp8_gated_round_and_a_few_tiles():
+    test_fp8_gated_every_variant(4200, 2048, 1152)
+
+
 def test_fp8_gemm_gated_saturated_gates():
     """Gates of thousands on both sides: sigma is exactly 0 or 1 there and nothing overflows to NaN."""
     fp8q = require_gpu()
