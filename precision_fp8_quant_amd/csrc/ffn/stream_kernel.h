@@ -72,18 +72,23 @@ __device__ __forceinline__ Frag load_frag(const uint8_t* row, int64_t k, int64_t
   return f;
 }
 
-template <bool INT8, bool GATED, int MF, int NF, int WAVES, int UNROLL, int OUT>
+// HALF (gated): a workgroup owns 8 columns of h; rows 0 .. 7 of a B fragment are
+// the gate's, rows 8 .. 15 the up projection's for the same columns.
+template <bool INT8, bool GATED, bool HALF, int MF, int NF, int WAVES, int UNROLL, int OUT>
 __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
-  constexpr int NP = GATED ? 2 : 1;               // projections
+  static_assert(!HALF || (GATED && NF == 1), "both projections in one fragment");
+  constexpr int NP = GATED && !HALF ? 2 : 1;      // fragments of B per column fragment
+  constexpr int NC = GATED ? 2 : 1;               // projections
+  constexpr int CW = HALF ? 8 : 16 * NF;          // columns per workgroup
   typedef typename std::conditional<INT8, v4i, v4f>::type acc_t;
   __shared__ acc_t part[WAVES][NP * MF][64];
-  __shared__ float s_sa[16 * MF], s_sb[NP * NF * 16], s_bias[NP * NF * 16];
+  __shared__ float s_sa[16 * MF], s_sb[NC * CW], s_bias[NC * CW];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lq = lane >> 4;
-  const int64_t ntiles = (p.N + 16 * NF - 1) / (16 * NF);
-  const int64_t n0 = (blockIdx.x % ntiles) * (16 * NF);
+  const int64_t ntiles = (p.N + CW - 1) / CW;
+  const int64_t n0 = (blockIdx.x % ntiles) * CW;
   const int64_t m0 = (blockIdx.x / ntiles) * (16 * MF);
 
   // Rows past the end repeat the last one: their products are not stored.
@@ -98,10 +103,10 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
   }
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
-    const int64_t c = n0 + 16 * f + lr;
+    const int64_t c = n0 + 16 * f + (HALF ? lr & 7 : lr);
     const int64_t n = c < p.N ? c : p.N - 1;
 #pragma unroll
-    for (int b = 0; b < NP; ++b) brow[b][f] = p.b + (b * p.up + n) * p.ldb + 16 * lq;
+    for (int b = 0; b < NP; ++b) brow[b][f] = p.b + ((HALF ? lr >> 3 : b) * p.up + n) * p.ldb + 16 * lq;
   }
 
   acc_t acc[NP][NF][MF];
@@ -132,7 +137,7 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
 #pragma unroll
       for (int i = 0; i < MF; ++i) x.sa[i] = p.sa[g * p.M + mrow[i]];
 #pragma unroll
-      for (int b = 0; b < NP; ++b) x.sb[b] = p.sb[((b * p.up + n0) >> 7) * KG + g];
+      for (int b = 0; b < NP; ++b) x.sb[b] = p.sb[(((HALF ? lq >> 1 : b) * p.up + n0) >> 7) * KG + g];
     }
   };
   auto use = [&](const Group& x) {
@@ -173,9 +178,9 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
   float my_sa = 0.0f, my_sb = 0.0f, my_bias = 0.0f;
   if constexpr (INT8) {
     if (p.K > 0 && tid < 16 * MF) my_sa = p.sa[m0 + tid < p.M ? m0 + tid : p.M - 1];
-    if (tid < NP * NF * 16) {
-      const int64_t c = n0 + tid % (NF * 16), n = c < p.N ? c : p.N - 1;
-      if (p.K > 0) my_sb = p.sb[tid / (NF * 16) * p.up + n];
+    if (tid < NC * CW) {
+      const int64_t c = n0 + tid % CW, n = c < p.N ? c : p.N - 1;
+      if (p.K > 0) my_sb = p.sb[tid / CW * p.up + n];
       if (!GATED && p.bias) my_bias = p.bias[n];
     }
   }
@@ -206,7 +211,7 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
 
   if constexpr (INT8) {
     if (tid < 16 * MF) s_sa[tid] = my_sa;
-    if (tid < NP * NF * 16) {
+    if (tid < NC * CW) {
       s_sb[tid] = my_sb;
       s_bias[tid] = my_bias;
     }
@@ -222,24 +227,26 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
       for (int i = 0; i < MF; ++i) part[wave][b * MF + i][lane] = acc[b][nf][i];
     __syncthreads();
     // Wave f adds the parts of row fragment f; a lane finishes four columns of
-    // one row.
-    if (wave < MF && m < p.M && n0 + 16 * nf + 4 * lq < p.N) {
+    // one row (HALF: of lane quarters 0 and 1; the up projection's values are
+    // 32 lanes above the gate's).
+    if (wave < MF && m < p.M && n0 + 16 * nf + 4 * lq < p.N && (!HALF || lq < 2)) {
       const int64_t n = n0 + 16 * nf + 4 * lq;
-      acc_t sum[NP];
+      acc_t sum[NC];
 #pragma unroll
-      for (int b = 0; b < NP; ++b) {
-        sum[b] = part[0][b * MF + wave][lane];
+      for (int b = 0; b < NC; ++b) {
+        const int part_b = HALF ? wave : b * MF + wave, part_lane = HALF ? lane + 32 * b : lane;
+        sum[b] = part[0][part_b][part_lane];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) sum[b] += part[w][b * MF + wave][lane];
+        for (int w = 1; w < WAVES; ++w) sum[b] += part[w][part_b][part_lane];
       }
       const int cols = p.N - n < 4 ? int(p.N - n) : 4;
-      float y[NP][4], out[4];
+      float y[NC][4], out[4];
 #pragma unroll
-      for (int b = 0; b < NP; ++b)
+      for (int b = 0; b < NC; ++b)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           y[b][j] = float(sum[b][j]);
-          if constexpr (INT8) y[b][j] *= s_sa[16 * wave + lr] * s_sb[b * (NF * 16) + 16 * nf + 4 * lq + j];
+          if constexpr (INT8) y[b][j] *= s_sa[16 * wave + lr] * s_sb[b * CW + 16 * nf + 4 * lq + j];
         }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -278,10 +285,11 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
   }
 }
 
-template <bool INT8, bool GATED, int OUT, int MF, int NF, int WAVES, int UNROLL>
+template <bool INT8, bool GATED, int OUT, int MF, int NF, int WAVES, int UNROLL, bool HALF = false>
 static hipError_t launch_stream_cfg(const FfnArgs& p, hipStream_t st) {
-  const int64_t tiles = ((p.N + 16 * NF - 1) / (16 * NF)) * ((p.M + 16 * MF - 1) / (16 * MF));
-  hipLaunchKernelGGL((stream_kernel<INT8, GATED, MF, NF, WAVES, UNROLL, OUT>), dim3(unsigned(tiles)), dim3(WAVES * 64),
+  constexpr int CW = HALF ? 8 : 16 * NF;
+  const int64_t tiles = ((p.N + CW - 1) / CW) * ((p.M + 16 * MF - 1) / (16 * MF));
+  hipLaunchKernelGGL((stream_kernel<INT8, GATED, HALF, MF, NF, WAVES, UNROLL, OUT>), dim3(unsigned(tiles)), dim3(WAVES * 64),
                      0, st, p);
   return hipGetLastError();
 }
@@ -300,15 +308,25 @@ static bool streams(const FfnArgs& p) {
   return p.M <= 16 || (p.M <= 32 && brows <= 24000) || (p.M <= 64 && brows > 5500 && brows <= 8600);
 }
 
-// 16 waves where there are fewer workgroups than CUs (FP8 gated 16x2048x7168
-// 12.2 us a call against 12.5), 8 otherwise (int8 1x7168x18432 26.0 against
+// 16 waves where there are no more workgroups than CUs (FP8 gated 16x2048x7168
+// by 16 columns 12.2 us a call against 12.5), 8 otherwise (int8 1x7168x18432 26.0 against
 // 29.8).  Two column fragments per wave halve what a plain product fetches of A
 // (int8 16x7168x18432 29.0 against 36.8), if they leave enough workgroups; a
 // gated one has its two projections already (FP8 16x18432x7168 56.8 with one,
-// 58.9 with two).
+// 58.9 with two).  Gated with at most 2048 columns, up to 32 rows: 8 columns a
+// workgroup, so that a CU streams half as much (us with 16 columns / with 8,
+// K = 7168: int8 1x2048 9.8 / 8.6, 16x2048 12.0 / 9.2, 32x2048 15.3 / 12.5,
+// 16x512 11.7 / 8.8; FP8 16x2048 12.1 / 9.9; with more columns than the CUs hold
+// at once it loses: int8 16x2688 12.1 / 16.1).  Eight of a plain product's
+// columns would leave half of each fragment empty, and gain nothing.
 template <bool INT8, bool GATED, int OUT>
 static hipError_t launch_stream(const FfnArgs& p, hipStream_t st) {
   const bool few = (p.N + 15) / 16 <= 256;
+  if constexpr (GATED) {
+    if ((p.N + 7) / 8 <= 256 && p.M <= 32)
+      return p.M <= 16 ? launch_stream_cfg<INT8, GATED, OUT, 1, 1, 16, 4, true>(p, st)
+                       : launch_stream_cfg<INT8, GATED, OUT, 2, 1, 16, 2, true>(p, st);
+  }
   if constexpr (!GATED) {
     if (p.M > 4 && (p.N + 31) / 32 >= 192) {
       if (p.M <= 16) return launch_stream_cfg<INT8, GATED, OUT, 1, 2, 8, 2>(p, st);

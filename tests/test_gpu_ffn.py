@@ -337,6 +337,17 @@ def test_int8_round_and_a_few_tiles(m, n, gated):
     test_int8_every_variant(m, n, 1101, gated)
 
 
+@pytest.mark.parametrize("m, f", [(1, 2048), (16, 2043), (17, 2041), (32, 2048), (32, 2049)])
+def test_int8_gated_eight_columns_a_workgroup(m, f):
+    """Up to 2048 columns, odd ones too: a workgroup has 8, gate and up in one fragment; 2049 are one too many."""
+    test_int8_every_variant(m, 2 * f, 1101, True)
+
+
+@pytest.mark.parametrize("m, f", [(1, 2048), (16, 1920), (17, 2048), (32, 1408)])
+def test_fp8_gated_eight_columns_a_workgroup(m, f):
+    test_fp8_gated_every_variant(m, f, 1152)
+
+
 def test_fp8_gated_round_and_a_few_tiles():
     test_fp8_gated_every_variant(4200, 2048, 1152)
 
