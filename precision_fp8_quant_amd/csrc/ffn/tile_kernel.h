@@ -441,7 +441,9 @@ static hipError_t launch_tile(const FfnArgs& p, hipStream_t st) {
   // first time up to 256 tiles and a line between the two beyond.  The time is
   // never less than the weight's 128 bytes a row take at the rate that each
   // tiling was seen to stream a weight too large for the caches: 2.8, 3.3, 2.5,
-  // 2.5 and 2.8 TB/s.  The smallest wins.  Measured (us, in the order above):
+  // 2.5 and 2.8 TB/s.  To this comes what a round takes to fill and to leave,
+  // 7.4, 3.4, 2.5, 1.6 and 1.5 us, half of it where half a CU's tiles are left.
+  // The smallest wins.  Measured (us, in the order above):
   //   int8  512x7168x7168   70  42  35  48  68
   //   int8  128x7168x7168   68  43  35  23  19
   //   int8 2048x7168x7168   80  96   -   -   -
@@ -450,21 +452,26 @@ static hipError_t launch_tile(const FfnArgs& p, hipStream_t st) {
   //   FP8 gated 512x2048x7168   80  44  35  26  36
   //   FP8 gated 1846x640x6016   70  38  32  41  47   (580 tiles of 64x64)
   //   FP8 gated 4096x1408x2048  33  36  43  52  77
+  //   FP8 gated 2056x14976x640  73  65   - 131   -
+  //   int8  333x2000x512      10.7 5.8 6.5 4.5 5.1
+  //   int8 1024x4096x512      11.4 6.9 7.6 9.9 16.7
+  //   int8 4096x4096x512        15  17  27  35  64
   const int64_t kg = (p.K + 127) / 128;
   const auto cost = [&](int64_t n, int i) {        // microseconds for n of the N columns in tiling i
-    struct Tiling { int64_t bm, bn, kw; float alone, full, tbs; };
-    constexpr Tiling tilings[5] = {{256, 256, 1, 1.24f, 1.24f, 2.8f}, {128, 128, 1, 0.75f, 0.49f, 3.3f},
-                                   {128, 128, 2, 0.61f, 0.61f, 2.5f}, {64, 64, 2, 0.40f, 0.25f, 2.5f},
-                                   {64, 64, 4, 0.33f, 0.33f, 2.8f}};
+    struct Tiling { int64_t bm, bn, kw; float alone, full, tbs, out; };
+    constexpr Tiling tilings[5] = {{256, 256, 1, 1.24f, 1.24f, 2.8f, 7.4f}, {128, 128, 1, 0.75f, 0.49f, 3.3f, 3.4f},
+                                   {128, 128, 2, 0.61f, 0.61f, 2.5f, 2.5f}, {64, 64, 2, 0.40f, 0.25f, 2.5f, 1.6f},
+                                   {64, 64, 4, 0.33f, 0.33f, 2.8f, 1.5f}};
     const Tiling& s = tilings[i];
     const int64_t cn = GATED ? s.bn / 2 : s.bn;
     const int64_t tiles = ((p.M + s.bm - 1) / s.bm) * ((n + cn - 1) / cn), two = s.alone != s.full ? 2 : 1;
     const int64_t last = tiles % (256 * two);
+    const float rounds = float(tiles / (256 * two));
     const float beyond = last > 256 ? float(last - 256) / 256.0f : 0.0f;
-    float c = float(tiles / (256 * two) * two) * s.full;
-    c += last ? s.alone + beyond * (2 * s.full - s.alone) : 0.0f;
+    const float c = rounds * float(two) * s.full + (last ? s.alone + beyond * (2 * s.full - s.alone) : 0.0f);
     const float stream = float(n * (GATED ? 2 : 1)) * 128e-6f / s.tbs;
-    return (c > stream ? c : stream) * float((kg + s.kw - 1) / s.kw * s.kw);
+    const float ends = rounds + (last > 256 || two == 1 ? float(last > 0) : last > 0 ? 0.5f : 0.0f);
+    return (c > stream ? c : stream) * float((kg + s.kw - 1) / s.kw * s.kw) + ends * s.out;
   };
   const auto pick = [&](int64_t n) {
     int best = 0;

@@ -330,6 +330,18 @@ def test_fp8_gated_every_variant(m, f, k):
     gu_intact()
 
 
+@pytest.mark.parametrize("m, n", [(500, 7000), (200, 1000)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_int8_teams_on_longer_k(m, n, gated):
+    """Two teams of waves in 128x128 tiles, four in 64x64: chosen from about 2000 on."""
+    test_int8_every_variant(m, n, 2300, gated)
+
+
+@pytest.mark.parametrize("m, f", [(500, 3584), (200, 512)])
+def test_fp8_gated_teams_on_longer_k(m, f):
+    test_fp8_gated_every_variant(m, f, 2304)
+
+
 @pytest.mark.parametrize("m, n", [(4200, 4059), (3300, 5700)])
 @pytest.mark.parametrize("gated", [False, True])
 def test_int8_round_and_a_few_tiles(m, n, gated):
