@@ -267,8 +267,8 @@ def test_fp8_gemm_gated_bf16(m, f, k):
 
 
 # Rows and columns for which each of the kernels' tilings and streaming variants is the one chosen: 256x256, 128x128 by
-# one team and 64x64 by two (128x128 by two and 64x64 by four on longer K, below); one, two and four row fragments, 16 waves, two column fragments; and a
-# last round of 256x256 tiles that runs as a problem of its own.
+# one team and 64x64 by two (128x128 by two and 64x64 by four on longer K, below); one, two and four row fragments, 16
+# waves, two column fragments; and a last round of 256x256 tiles that runs as a problem of its own.
 VARIANTS = [(2040, 17348), (2000, 5300), (1300, 5000), (500, 7000), (500, 3000), (200, 1000), (3, 5000), (9, 6200), (30, 6200),
             (40, 6200), (30, 3000), (20, 8000), (60, 8000), (40, 3000)]
 
