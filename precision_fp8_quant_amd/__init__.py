@@ -17,8 +17,14 @@ Functions keep the C names:
 and, from include/fp8q_ffn.h (module ``ffn``), the gated feed-forward operators fp8_gemm_gated, fp8_gated_backward,
 int8_quant_rows, int8_gemm and int8_gemm_gated.
 FP8 tensors are torch.uint8 holding OCP E4M3FN codes.
+
+stream= takes a torch stream or a raw handle; without it a call goes to the current stream of the tensors' device.
+Outputs that a call allocates are allocated on the stream it goes to, so the next call on that stream may drop them at
+once.  As with torch's own operations, inputs and outputs that belong to another stream are the caller's to order
+(wait_stream) and to keep until that work is done (record_stream).
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -89,17 +95,36 @@ def _check(status):
         raise Fp8qError(status)
 
 
+def _handle(stream, dev):
+    """The raw handle of a caller's stream."""
+    if isinstance(getattr(stream, "device", None), torch.device) and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_AS_IT_IS = contextlib.nullcontext()
+
+
+def _outputs_on(stream, dev):
+    """Context in which the outputs of a call on `stream` are allocated.  torch's allocator hands a freed block out
+    again in the order of the stream that it was allocated on: an output that was allocated on the current stream
+    and is written on another one could still be in use there, or be handed out while the kernel writes it."""
+    if stream is None:
+        return _AS_IT_IS
+    handle = _handle(stream, dev)
+    if handle == torch._C._cuda_getCurrentRawStream(dev.index):
+        return _AS_IT_IS
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
 def _run(fn, dev, stream, *args):
     """Call entry point `fn` with the tensors' device `dev` current and the stream resolved on it: the kernels run
     on the stream's device, and the NULL stream (torch's default stream) is the current device's.  Where `dev` is
     current already, as it nearly always is, no device guard is set up and the current stream's handle is asked for
     directly: a small int8_gemm call took 15.8 us and takes 9.5, of which the launch is 3."""
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev.index)
-    else:
-        if isinstance(getattr(stream, "device", None), torch.device) and stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _handle(stream, dev)
     if torch._C._cuda_getDevice() == dev.index:
         status = fn(*args, handle)
     else:
@@ -170,10 +195,11 @@ def fp8_quant_tile(x, tile=TILE_1x128, mode=MAXABS, q=None, scales=None, stream=
     rows, cols = x.shape
     q_shape = (rows, cols) if tile == TILE_1x128 else (cols, rows)
     s_shape = (_cdiv(cols, 128), rows) if tile == TILE_1x128 else (_cdiv(rows, 128), cols)
-    if q is None:
-        q = torch.empty(q_shape, dtype=torch.uint8, device=x.device)
-    if scales is None:
-        scales = torch.empty(s_shape, dtype=torch.float32, device=x.device)
+    with _outputs_on(stream, x.device):
+        if q is None:
+            q = torch.empty(q_shape, dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty(s_shape, dtype=torch.float32, device=x.device)
     q = _expect(_codes(q), "q", torch.uint8, q_shape, x.device)
     _expect(scales, "scales", torch.float32, s_shape, x.device, dense=True)
     _run(lib.fp8_quant_tile, x.device, stream, x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), tile, mode,
@@ -187,14 +213,15 @@ def fp8_quant_tile_dual(x, mode=MAXABS, q=None, scales=None, q_t=None, scales_t=
     _rowmajor(x, "x")
     rows, cols = x.shape
     dev = x.device
-    if q is None:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-    if scales is None:
-        scales = torch.empty((_cdiv(cols, 128), rows), dtype=torch.float32, device=dev)
-    if q_t is None:
-        q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev)
-    if scales_t is None:
-        scales_t = torch.empty((_cdiv(rows, 128), cols), dtype=torch.float32, device=dev)
+    with _outputs_on(stream, dev):
+        if q is None:
+            q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty((_cdiv(cols, 128), rows), dtype=torch.float32, device=dev)
+        if q_t is None:
+            q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev)
+        if scales_t is None:
+            scales_t = torch.empty((_cdiv(rows, 128), cols), dtype=torch.float32, device=dev)
     q = _expect(_codes(q), "q", torch.uint8, (rows, cols), dev)
     _expect(scales, "scales", torch.float32, (_cdiv(cols, 128), rows), dev, dense=True)
     q_t = _expect(_codes(q_t), "q_t", torch.uint8, (cols, rows), dev)
@@ -213,15 +240,16 @@ def fp8_quant_block(w, mode=MAXABS, transposed=False, q=None, scales=None, q_t=N
     dev = w.device
     if not transposed and (q_t is not None or scales_t is not None):
         raise ValueError("q_t / scales_t are the transposed copy: pass transposed=True")
-    if q is None:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-    if scales is None:
-        scales = torch.empty((rows // 128, cols // 128), dtype=torch.float32, device=dev)
-    if transposed:
-        if q_t is None:
-            q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev)
-        if scales_t is None:
-            scales_t = torch.empty((cols // 128, rows // 128), dtype=torch.float32, device=dev)
+    with _outputs_on(stream, dev):
+        if q is None:
+            q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty((rows // 128, cols // 128), dtype=torch.float32, device=dev)
+        if transposed:
+            if q_t is None:
+                q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev)
+            if scales_t is None:
+                scales_t = torch.empty((cols // 128, rows // 128), dtype=torch.float32, device=dev)
     q = _expect(_codes(q), "q", torch.uint8, (rows, cols), dev)
     _expect(scales, "scales", torch.float32, (_cdiv(rows, 128), _cdiv(cols, 128)), dev, dense=True)
     if q_t is not None:
@@ -265,7 +293,8 @@ def _gemm(fn, kind, a, a_scales, b, b_scales, out_dtype, c, accumulate, stream, 
         sb_shape = (_cdiv(k, 128), n) if kind == WGRAD else (_cdiv(n, 128), _cdiv(k, 128))
         _expect(b_scales, "b_scales", torch.float32, sb_shape, dev, dense=True)
     if c is None:
-        c = torch.empty((m, n), dtype=out_dtype, device=dev)
+        with _outputs_on(stream, dev):
+            c = torch.empty((m, n), dtype=out_dtype, device=dev)
     if c.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"c must be bfloat16 or float32, got {c.dtype}")
     _expect(c, "c", c.dtype, (m, n), dev)
@@ -292,7 +321,8 @@ def fp8_gemm_blockscaled_grouped(group_of_mtile, a, a_scales, b, b_scales, out_d
     _expect(a_scales, "a_scales", torch.float32, (_cdiv(k, 128), m), dev, dense=True)
     _expect(b_scales, "b_scales", torch.float32, (g, _cdiv(n, 128), _cdiv(k, 128)), dev, dense=True)
     if c is None:
-        c = torch.empty((m, n), dtype=out_dtype, device=dev)
+        with _outputs_on(stream, dev):
+            c = torch.empty((m, n), dtype=out_dtype, device=dev)
     if c.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"c must be bfloat16 or float32, got {c.dtype}")
     _expect(c, "c", c.dtype, (m, n), dev)
@@ -308,10 +338,11 @@ def fp8_requant_1x128_to_128x1(q, scales, mode=POW2, q_t=None, scales_t=None, st
     rows, cols = q.shape
     dev = q.device
     _expect(scales, "scales", torch.float32, (_cdiv(cols, 128), rows), dev, dense=True)
-    if q_t is None:
-        q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev)
-    if scales_t is None:
-        scales_t = torch.empty((_cdiv(rows, 128), cols), dtype=torch.float32, device=dev)
+    with _outputs_on(stream, dev):
+        if q_t is None:
+            q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev)
+        if scales_t is None:
+            scales_t = torch.empty((_cdiv(rows, 128), cols), dtype=torch.float32, device=dev)
     q_t = _expect(_codes(q_t), "q_t", torch.uint8, (cols, rows), dev)
     _expect(scales_t, "scales_t", torch.float32, (_cdiv(rows, 128), cols), dev, dense=True)
     _run(lib.fp8_requant_1x128_to_128x1, dev, stream, q.data_ptr(), rows, cols, _ld(q), scales.data_ptr(), mode,
