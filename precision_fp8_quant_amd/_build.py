@@ -36,7 +36,7 @@ PER_SOURCE_FLAGS = {"gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 
 
 # The native call path of ffn.py: a CPython extension against torch's headers,
-# linked to libfp8q.so beside it.
+# linked to libfp8q.so beside it.  The package works without it.
 BINDING_SRC = os.path.join(CSRC, "ffn", "binding.cpp")
 BINDING_PATH = os.path.join(PKG_DIR, "_ffn_call.so")
 
@@ -72,8 +72,8 @@ def _run(cmd, verbose):
     return res
 
 
-def build(verbose=False, extra_flags=()):
-    """Compile every source and link libfp8q.so and the native call path (always recompiles)."""
+def build_library(verbose=False, extra_flags=()):
+    """Compile every source and link libfp8q.so, which needs nothing but hipcc."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = []
     for src in DEVICE_SOURCES:
@@ -84,13 +84,29 @@ def build(verbose=False, extra_flags=()):
         obj = os.path.join(BUILD_DIR, src.replace("/", "_") + ".o")
         jobs.append([HIPCC, *COMMON_FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj])
     objs = [j[-1] for j in jobs]
-    binding = os.path.join(BUILD_DIR, "ffn_binding.cpp.o")
-    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
-        list(ex.map(lambda c: _run(c, verbose), [*jobs, _binding_command(binding)]))
+    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+        list(ex.map(lambda c: _run(c, verbose), jobs))
     tmp = LIB_PATH + ".tmp"
     _run([HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB_PATH)
-    _link_binding(binding, verbose)
+    return LIB_PATH
+
+
+def build(verbose=False, extra_flags=()):
+    """libfp8q.so and, where torch is installed, the native call path (always recompiles).  The library is complete
+    when the call path fails to build, which is still an error."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    binding = os.path.join(BUILD_DIR, "ffn_binding.cpp.o")
+    with ThreadPoolExecutor(max_workers=1) as ex:  # beside the library's sources
+        try:
+            compiled = ex.submit(_run, _binding_command(binding), verbose)
+        except ImportError as e:
+            compiled = None
+            print(f"{os.path.basename(BINDING_PATH)} is not built: {e}", flush=True)
+        build_library(verbose, extra_flags)
+    if compiled:
+        compiled.result()
+        _link_binding(binding, verbose)
     return LIB_PATH
 
 

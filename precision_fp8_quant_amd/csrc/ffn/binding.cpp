@@ -18,6 +18,7 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 namespace {
 
@@ -227,4 +228,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ffn_call", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__ffn_call(void) { return PyModule_Create(&module); }
+// torch_version: what the tensors' layout was compiled for; ffn.py compares it.
+PyMODINIT_FUNC PyInit__ffn_call(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}

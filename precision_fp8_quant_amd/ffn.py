@@ -13,11 +13,35 @@ no multiple of 16 bytes comes back as a view of wider rows.
 """
 
 import ctypes
+import os
+import warnings
 
 import torch
 
 from . import BF16, F32, MAXABS, OK, _cdiv, _check, _codes, _expect, _i64, _int, _outputs_on, _ptr, _rowmajor, _run, lib
-from . import _ffn_call as _native
+
+_NATIVE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_ffn_call.so")
+
+
+def _load_native():
+    """The native call path, or None where it was not built or was built for another torch: every call works without
+    it, through ctypes and with more host time."""
+    if not os.path.exists(_NATIVE_PATH):
+        return None
+    try:
+        from . import _ffn_call
+    except ImportError as e:
+        why = str(e)
+    else:
+        if _ffn_call.torch_version == torch.__version__.split("+")[0]:
+            return _ffn_call
+        why = f"built for torch {_ffn_call.torch_version}, this is {torch.__version__}"
+    warnings.warn(f"{_NATIVE_PATH} is not used: {why}. Rebuild it with __graft_entry__.build(); until then calls of the "
+                  "gated feed-forward operators take more host time", RuntimeWarning, stacklevel=3)
+    return None
+
+
+_native = _load_native()
 
 # enum of include/fp8q_ffn.h
 ACT_SILU, ACT_GELU_TANH = 0, 1
@@ -118,7 +142,7 @@ def fp8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bfloa
     """h[M][F] = act(A Bg^T) * (A Bu^T) from block-scaled FP8 operands: a [M][K] in 1x128 tiles, b [2F][K] the stacked
     gate and up weights in 128x128 blocks.  With save_gate_up=True (or a gu tensor) also gu[M][2F], the
     pre-activations that fp8_gated_backward takes."""
-    if h is None and gu is None and stream is None:
+    if _native and h is None and gu is None and stream is None:
         r = _native.fp8_gemm_gated(a, a_scales, b, b_scales, act, _CODE.get(out_dtype), save_gate_up)
         if r is not None:
             return _done(r)
@@ -151,7 +175,7 @@ def fp8_gated_backward(dh, gu, act=ACT_SILU, mode=MAXABS, q=None, scales=None, q
     1x128 tiles (q [Mp][2F], scales [2F/128][Mp]: Dgrad's operand) and transposed 128x1 tiles (q_t [2F][Mp],
     scales_t [Mp/128][2F]: Wgrad's), Mp being M rounded up to whole 128-row tiles and the rows past M zero.  A dgu
     tensor [M][2F] also receives D itself."""
-    if q is None and scales is None and q_t is None and scales_t is None and dgu is None and stream is None:
+    if _native and q is None and scales is None and q_t is None and scales_t is None and dgu is None and stream is None:
         r = _native.fp8_gated_backward(dh, gu, act, mode)
         if r is not None:
             return _done(r)
@@ -186,7 +210,7 @@ def fp8_gated_backward(dh, gu, act=ACT_SILU, mode=MAXABS, q=None, scales=None, q
 def int8_quant_rows(x, q=None, scales=None, stream=None):
     """Symmetric 8-bit codes of a 2-D bf16/fp32 tensor with one scale for each row (token or output channel):
     q int8 [rows][cols], scales [rows], x ~= q * scales[:, None]."""
-    if q is None and scales is None and stream is None:
+    if _native and q is None and scales is None and stream is None:
         r = _native.int8_quant_rows(x)
         if r is not None:
             return _done(r)
@@ -213,7 +237,7 @@ def int8_quant_rows(x, q=None, scales=None, stream=None):
 
 def int8_gemm(a, a_scales, b, b_scales, bias=None, out_dtype=torch.bfloat16, c=None, stream=None):
     """C[M][N] = a_scales[m] * b_scales[n] * (A . B^T) (+ bias[n]) from 8-bit integers a [M][K] and b [N][K]."""
-    if c is None and stream is None:
+    if _native and c is None and stream is None:
         r = _native.int8_gemm(a, a_scales, b, b_scales, bias, _CODE.get(out_dtype))
         if r is not None:
             return _done(r)
@@ -234,7 +258,7 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, out_dtype=torch.bfloat16, c=N
 def int8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bfloat16, h=None, stream=None):
     """h[M][F] = act(g) * u with g and u the int8_gemm products of a [M][K] and the stacked gate and up weights
     b [2F][K]."""
-    if h is None and stream is None:
+    if _native and h is None and stream is None:
         r = _native.int8_gemm_gated(a, a_scales, b, b_scales, act, _CODE.get(out_dtype))
         if r is not None:
             return _done(r)
