@@ -8,6 +8,14 @@
 
 namespace fp8q {
 
+// HIP takes launches of fewer than 2^32 threads.
+constexpr int64_t max_grid(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
+
+// Workgroups for `units` of them: kernels with a loop over the grid do what is left in further rounds.
+inline unsigned grid_of(int64_t units, int threads) {
+  return unsigned(units < max_grid(threads) ? units : max_grid(threads));
+}
+
 // One product (or gated pair of products) of K-contiguous 8-bit operands.
 struct FfnArgs {
   const uint8_t* a; int64_t lda; const float* sa;

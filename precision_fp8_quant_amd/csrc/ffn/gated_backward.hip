@@ -214,8 +214,7 @@ hipError_t launch_gated_backward(float act_c1, float act_c3, int64_t M, int64_t 
                                  float* scales, uint8_t* q_t, int64_t ld_qt, float* scales_t, void* dgu,
                                  int64_t ld_dgu, hipStream_t st) {
   const BwdArgs p{M, F, ld_dh, ld_gu, q, ld_q, scales, q_t, ld_qt, scales_t, ld_dgu, act_c1, act_c3};
-  const int64_t blocks = (F / 128) * ((M + 127) / 128);
-  const dim3 grid(unsigned(blocks < 0x7FFFFFFF ? blocks : 0x7FFFFFFF));
+  const dim3 grid(grid_of((F / 128) * ((M + 127) / 128), 512));
   auto go = [&](auto kernel, auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
     hipLaunchKernelGGL(kernel, grid, dim3(512), 0, st, static_cast<const T*>(dh), static_cast<const T*>(gu),

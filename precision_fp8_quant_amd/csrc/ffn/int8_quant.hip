@@ -134,8 +134,8 @@ hipError_t launch_cfg(const T* x, int64_t rows, int64_t cols, int64_t ld_x, int8
                       hipStream_t st) {
   constexpr int RPB = 256 / TPR;
   const int64_t blocks = (rows - 1) / RPB + 1;
-  hipLaunchKernelGGL((int8_quant_rows_kernel<T, TPR, R>), dim3(unsigned(blocks < 0x7FFFFFFF ? blocks : 0x7FFFFFFF)),
-                     dim3(256), 0, st, x, rows, cols, ld_x, q, ld_q, scales);
+  hipLaunchKernelGGL((int8_quant_rows_kernel<T, TPR, R>), dim3(grid_of(blocks, 256)), dim3(256), 0, st, x, rows, cols, ld_x,
+                     q, ld_q, scales);
   return hipGetLastError();
 }
 
