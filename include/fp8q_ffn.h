@@ -52,8 +52,9 @@ typedef enum { FP8Q_ACT_SILU = 0, FP8Q_ACT_GELU_TANH = 1 } fp8q_act;
  *            out_dtype: g in columns [0, F), u in columns [F, 2F), each
  *            rounded once from FP32 -- what fp8_gated_backward takes.  h is
  *            formed from the unrounded g and u.
- * Requires F and K multiples of 128, lda and ldb of at most 4,194,176 bytes
- * (FP8Q_ERR_UNSUPPORTED).  M == 0 or F == 0 is a no-op; K == 0 writes zeros.
+ * Requires F and K multiples of 128, lda and ldb of at most 4,194,176 bytes,
+ * at most 2^31-1 tiles of 16x16 in h (FP8Q_ERR_UNSUPPORTED).  M == 0 or F == 0
+ * is a no-op; K == 0 writes zeros.
  */
 int fp8_gemm_gated(int act, int64_t M, int64_t F, int64_t K,
                    const uint8_t* a, int64_t lda, const float* a_scales,
@@ -127,9 +128,9 @@ int int8_quant_rows(const void* x, int x_dtype, int64_t rows, int64_t cols, int6
  * readable in every row, the last one included, and the bytes between one row
  * and the next may be read; their values do not matter.
  * Every code from -128 to 127 is allowed.  K of at most 131,056 (beyond it the
- * 32-bit sum could overflow) and lda, ldb of at most 4,194,176 bytes;
- * otherwise FP8Q_ERR_UNSUPPORTED.  M == 0 or N == 0 is a no-op; K == 0 writes
- * the bias or zeros.
+ * 32-bit sum could overflow), lda, ldb of at most 4,194,176 bytes and at most
+ * 2^31-1 tiles of 16x16 in C; otherwise FP8Q_ERR_UNSUPPORTED.  M == 0 or
+ * N == 0 is a no-op; K == 0 writes the bias or zeros.
  */
 int int8_gemm(int64_t M, int64_t N, int64_t K,
               const int8_t* a, int64_t lda, const float* a_scales,

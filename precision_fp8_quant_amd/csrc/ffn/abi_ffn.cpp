@@ -44,7 +44,8 @@ int check_ranges(const Range (&outs)[NO], const Range (&ins)[NI]) {
   return FP8Q_OK;
 }
 
-// Tiles of the smallest kind (16 x 16) beyond one grid.
+// More outputs than a card's memory holds, as 16 x 16 tiles: up to here sizes and tile numbers stay far from overflow.
+// (Products of more tiles than one launch takes are cut up, ffn_launch.h.)
 bool grid_ok(int64_t M, int64_t N) {
   const int64_t tm = (M - 1) / 16 + 1, tn = (N - 1) / 16 + 1;
   return tn <= kMaxGridX / tm;
@@ -101,7 +102,7 @@ int fp8_gemm_gated(int act, int64_t M, int64_t F, int64_t K, const uint8_t* a, i
                         span(b_scales, k0 ? 0 : 1, nsb, nsb, 4)};
   const int bad = check_ranges(outs, ins);
   if (bad != FP8Q_OK) return bad;
-  fp8q::FfnArgs p{a, lda, a_scales, b, ldb, b_scales, nullptr, h, ldh, gu, ldgu, M, F, K, F, 0.0f, 0.0f};
+  fp8q::FfnArgs p{a, lda, a_scales, b, ldb, b_scales, nullptr, h, ldh, gu, ldgu, M, F, K, F, 0.0f, 0.0f, M};
   set_act(act, &p.act_c1, &p.act_c3);
   return from_hip(fp8q::launch_fp8_gated(p, out_dtype == FP8Q_BF16, reinterpret_cast<hipStream_t>(stream)));
 }
@@ -163,7 +164,7 @@ int int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, con
   const int bad = check_int8(M, N, K, N, a, lda, a_scales, b, ldb, b_scales, bias, c, c_dtype, ldc);
   if (bad != FP8Q_OK) return bad;
   const fp8q::FfnArgs p{reinterpret_cast<const uint8_t*>(a), lda, a_scales, reinterpret_cast<const uint8_t*>(b), ldb,
-                        b_scales, bias, c, ldc, nullptr, 0, M, N, K, 0, 0.0f, 0.0f};
+                        b_scales, bias, c, ldc, nullptr, 0, M, N, K, 0, 0.0f, 0.0f, 0};
   return from_hip(fp8q::launch_int8_gemm(p, c_dtype == FP8Q_BF16, reinterpret_cast<hipStream_t>(stream)));
 }
 
@@ -178,7 +179,7 @@ int int8_gemm_gated(int act, int64_t M, int64_t F, int64_t K, const int8_t* a, i
   const int bad = check_int8(M, F, K, f2, a, lda, a_scales, b, ldb, b_scales, nullptr, h, out_dtype, ldh);
   if (bad != FP8Q_OK) return bad;
   fp8q::FfnArgs p{reinterpret_cast<const uint8_t*>(a), lda, a_scales, reinterpret_cast<const uint8_t*>(b), ldb,
-                  b_scales, nullptr, h, ldh, nullptr, 0, M, F, K, F, 0.0f, 0.0f};
+                  b_scales, nullptr, h, ldh, nullptr, 0, M, F, K, F, 0.0f, 0.0f, 0};
   set_act(act, &p.act_c1, &p.act_c3);
   return from_hip(fp8q::launch_int8_gated(p, out_dtype == FP8Q_BF16, reinterpret_cast<hipStream_t>(stream)));
 }

@@ -3,18 +3,12 @@
 // the launch status without synchronising.
 #pragma once
 
+#include "launch_plan.h"
+
 #include <hip/hip_runtime_api.h>
 #include <stdint.h>
 
 namespace fp8q {
-
-// HIP takes launches of fewer than 2^32 threads.
-constexpr int64_t max_grid(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
-
-// Workgroups for `units` of them: kernels with a loop over the grid do what is left in further rounds.
-inline unsigned grid_of(int64_t units, int threads) {
-  return unsigned(units < max_grid(threads) ? units : max_grid(threads));
-}
 
 // One product (or gated pair of products) of K-contiguous 8-bit operands.
 struct FfnArgs {
@@ -26,7 +20,40 @@ struct FfnArgs {
   int64_t M, N, K;                // N: columns of c (F where the product is gated)
   int64_t up;                     // gated: rows of b (scales, columns of gu) from the gate's to the up's
   float act_c1, act_c3;           // the activation's sigma argument (gate_act.h)
+  int64_t sa_ld;                  // FP8: scales of A from one K-group to the next
 };
+
+// Rows [m0, m0 + rows) and columns [n0, n0 + cols) of a product; n0 in whole 128 columns where the operands are FP8.
+inline FfnArgs part_of(const FfnArgs& p, bool int8, bool out_bf16, int64_t m0, int64_t rows, int64_t n0, int64_t cols) {
+  const int64_t es = out_bf16 ? 2 : 4;
+  FfnArgs q = p;
+  q.M = rows;
+  q.N = cols;
+  if (p.K > 0) {                  // otherwise there may be no operands
+    q.a = p.a + m0 * p.lda;
+    q.sa = p.sa + m0;
+    q.b = p.b + n0 * p.ldb;
+    q.sb = p.sb + (int8 ? n0 : n0 / 128 * ((p.K + 127) / 128));
+  }
+  if (p.bias) q.bias = p.bias + n0;
+  q.c = static_cast<uint8_t*>(p.c) + (m0 * p.ldc + n0) * es;
+  if (p.gu) q.gu = static_cast<uint8_t*>(p.gu) + (m0 * p.ldgu + n0) * es;
+  return q;
+}
+
+// launch(part, workgroups) for the whole product in tiles of bm x bn, as many times as the grid's limit asks for.
+template <typename Launch>
+hipError_t in_pieces(const FfnArgs& p, bool int8, bool out_bf16, int64_t bm, int64_t bn, int threads, Launch launch) {
+  const Piece s = piece_size(p.M, p.N, bm, bn, threads);
+  for (int64_t m0 = 0; m0 < p.M; m0 += s.rows)
+    for (int64_t n0 = 0; n0 < p.N; n0 += s.cols) {
+      const int64_t rows = p.M - m0 < s.rows ? p.M - m0 : s.rows, cols = p.N - n0 < s.cols ? p.N - n0 : s.cols;
+      const hipError_t e = launch(part_of(p, int8, out_bf16, m0, rows, n0, cols),
+                                  unsigned(((rows + bm - 1) / bm) * ((cols + bn - 1) / bn)));
+      if (e != hipSuccess) return e;
+    }
+  return hipSuccess;
+}
 
 hipError_t launch_fp8_gated(const FfnArgs& p, bool out_bf16, hipStream_t st);
 hipError_t launch_int8_gemm(const FfnArgs& p, bool out_bf16, hipStream_t st);

@@ -135,7 +135,7 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
     for (int i = 0; i < MF; ++i) x.a[i] = load_frag<TAIL, TAIL>(arow[i], g * 128, left);
     if constexpr (!INT8) {
 #pragma unroll
-      for (int i = 0; i < MF; ++i) x.sa[i] = p.sa[g * p.M + mrow[i]];
+      for (int i = 0; i < MF; ++i) x.sa[i] = p.sa[g * p.sa_ld + mrow[i]];
 #pragma unroll
       for (int b = 0; b < NP; ++b) x.sb[b] = p.sb[(((HALF ? lq >> 1 : b) * p.up + n0) >> 7) * KG + g];
     }
@@ -287,11 +287,11 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
 
 template <bool INT8, bool GATED, int OUT, int MF, int NF, int WAVES, int UNROLL, bool HALF = false>
 static hipError_t launch_stream_cfg(const FfnArgs& p, hipStream_t st) {
-  constexpr int CW = HALF ? 8 : 16 * NF;
-  const int64_t tiles = ((p.N + CW - 1) / CW) * ((p.M + 16 * MF - 1) / (16 * MF));
-  hipLaunchKernelGGL((stream_kernel<INT8, GATED, HALF, MF, NF, WAVES, UNROLL, OUT>), dim3(unsigned(tiles)), dim3(WAVES * 64),
-                     0, st, p);
-  return hipGetLastError();
+  return in_pieces(p, INT8, OUT == kOutBF16, 16 * MF, HALF ? 8 : 16 * NF, WAVES * 64, [&](const FfnArgs& q, unsigned grid) {
+    hipLaunchKernelGGL((stream_kernel<INT8, GATED, HALF, MF, NF, WAVES, UNROLL, OUT>), dim3(grid), dim3(WAVES * 64), 0, st,
+                       q);
+    return hipGetLastError();
+  });
 }
 
 // Whether streaming beats the LDS tiles (tile_kernel.h).  Beyond 16 rows every

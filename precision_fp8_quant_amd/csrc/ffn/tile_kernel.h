@@ -69,7 +69,7 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
 
   // ---- tile scheduling: every XCD (workgroup i runs on XCD i % 8) gets one
   // contiguous range of tiles, in groups of 8 tiles along M ------------------
-  // (The grid has fewer than 2^31 workgroups, so tile numbers are 32-bit.  They
+  // (The grid has fewer than 2^24 workgroups, so tile numbers are 32-bit.  They
   // are made provably wave-uniform: buffer resources built from values that the
   // compiler holds to be divergent turn every DMA into a loop over the lanes.)
   const uint32_t tiles_m = uint32_t((p.M + BM - 1) / BM);
@@ -142,7 +142,7 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
       uint8_t* const s = smem + stage * STAGE + A_BYTES + B_BYTES;
       if (wave < BM / 64) {
         const int row = 64 * wave + lane;
-        const float* src = p.sa + g * p.M + m0 + (row < mrows ? row : mrows - 1);
+        const float* src = p.sa + g * p.sa_ld + m0 + (row < mrows ? row : mrows - 1);
         __builtin_amdgcn_global_load_lds((gptr_t)src, (lptr_t)(s + 256 * wave), 4, 0, 0);
       }
       if (wave == NW - 1 && lane < 2) {
@@ -412,11 +412,11 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
 
 template <bool INT8, bool GATED, int OUT, int BM, int BN, int WM, int PF, int STAGES, int KW>
 static hipError_t launch_tile_cfg(const FfnArgs& p, hipStream_t st) {
-  constexpr int CN = GATED ? BN / 2 : BN;
-  const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.N + CN - 1) / CN);
-  hipLaunchKernelGGL((tile_kernel<INT8, GATED, BM, BN, WM, PF, STAGES, KW, OUT>), dim3(unsigned(tiles)),
-                     dim3(KW * WM * (BN / (32 * PF)) * 64), 0, st, p);
-  return hipGetLastError();
+  constexpr int THREADS = KW * WM * (BN / (32 * PF)) * 64;
+  return in_pieces(p, INT8, OUT == kOutBF16, BM, GATED ? BN / 2 : BN, THREADS, [&](const FfnArgs& q, unsigned grid) {
+    hipLaunchKernelGGL((tile_kernel<INT8, GATED, BM, BN, WM, PF, STAGES, KW, OUT>), dim3(grid), dim3(THREADS), 0, st, q);
+    return hipGetLastError();
+  });
 }
 
 template <bool INT8, bool GATED, int OUT>
@@ -488,16 +488,10 @@ static hipError_t launch_tile(const FfnArgs& p, hipStream_t st) {
   const int64_t tm = (p.M + 255) / 256, tn = (p.N + CN - 1) / CN;
   const int64_t whole = tm * tn / 256 * 256 / tm;  // such columns
   if (whole > 0 && whole < tn) {
-    const int64_t cut = whole * CN, es = OUT == kOutBF16 ? 2 : 4;
+    const int64_t cut = whole * CN;
     if (cost(cut, 0) + cost(p.N - cut, pick(p.N - cut)) + 3.0f < cost(p.N, best)) {
-      FfnArgs head = p, rest = p;
-      head.N = cut;
-      rest.N = p.N - cut;
-      rest.b = p.b + cut * p.ldb;
-      rest.sb = p.sb + (INT8 ? cut : cut / 128 * kg);
-      rest.bias = p.bias ? p.bias + cut : nullptr;
-      rest.c = static_cast<uint8_t*>(p.c) + cut * es;
-      rest.gu = p.gu ? static_cast<uint8_t*>(p.gu) + cut * es : nullptr;
+      const FfnArgs head = part_of(p, INT8, OUT == kOutBF16, 0, p.M, 0, cut);
+      const FfnArgs rest = part_of(p, INT8, OUT == kOutBF16, 0, p.M, cut, p.N - cut);
       const hipError_t e = launch_tile_cfg<INT8, GATED, OUT, 256, 256, 4, 4, 2, 1>(head, st);
       return e != hipSuccess ? e : launch_tile<INT8, GATED, OUT>(rest, st);
     }

@@ -30,3 +30,58 @@ def test_int8_quant_rows_beyond_one_grid(rows, cols):
         assert torch.equal(q[r:r + n], want_q[same]) and torch.equal(s[r:r + n], want_s[same]), r
     del x, q, s
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("m, n, gated", [(1, (1 << 27) + 40, False), (3, (1 << 27) + 24, True), (9, (1 << 28) + 200, False)])
+def test_int8_products_of_more_columns_than_one_launch_takes(m, n, gated):
+    """The streaming kernel's launches are cut along N (16 codes deep; 2^27 columns in workgroups of 16, 2^28 of 32)."""
+    fp8q = require_gpu()
+    k, part, rows = 16, 1 << 24, 2 * n if gated else n
+    gen = torch.Generator(device="cuda").manual_seed(n % 1000)
+    a = torch.randint(-128, 128, (m, k), generator=gen, device="cuda", dtype=torch.int8)
+    b = torch.randint(-128, 128, (rows, k), generator=gen, device="cuda", dtype=torch.int8)
+    sa = torch.rand(m, generator=gen, device="cuda") * 1e-4 + 1e-5
+    sb = torch.rand(rows, generator=gen, device="cuda") + 0.5
+    if gated:
+        got = fp8q.int8_gemm_gated(a, sa, b, sb, out_dtype=torch.float32)
+    else:
+        bias = torch.randn(n, generator=gen, device="cuda")
+        got = fp8q.int8_gemm(a, sa, b, sb, bias=bias, out_dtype=torch.float32)
+    for c in range(0, n, part):
+        e = min(n, c + part)
+        y = lambda lo: (a.double() @ b[lo + c:lo + e].double().t()) * sa.double()[:, None] * sb[lo + c:lo + e].double()  # noqa: E731
+        # the tolerances of tests/test_gpu_ffn.py: the scaled sum to 4 units, the gated product to 22 + 20 |g|
+        if gated:
+            g, u = y(0), y(n)
+            ref = g * torch.sigmoid(g) * u
+            tol = (22 + 20 * g.abs()) * 2.0 ** -24 * ref.abs() + 2.0 ** -100 * (1 + (g * u).abs())
+        else:
+            prod = y(0)
+            ref = prod + bias[c:e].double()
+            tol = 4 * 2.0 ** -24 * (prod.abs() + ref.abs()) + 2.0 ** -100
+        assert bool(((got[:, c:e].double() - ref).abs() <= tol).all()), c
+    del b, got
+    torch.cuda.empty_cache()
+
+
+def test_int8_product_of_more_rows_than_one_launch_takes():
+    """2^31 + 3 rows of one column: the tiled kernel's launches are cut along M."""
+    fp8q = require_gpu()
+    m, n, k, part = (1 << 31) + 3, 1, 16, 1 << 26
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    base = torch.randint(-128, 128, (part + 7, k), generator=gen, device="cuda", dtype=torch.int8)
+    scale = torch.rand(part + 7, generator=gen, device="cuda") + 0.5
+    a, sa = torch.empty((m, k), dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    b = torch.randint(-128, 128, (n, k), generator=gen, device="cuda", dtype=torch.int8)
+    sb = torch.rand(n, generator=gen, device="cuda") + 0.5
+    for i, r in enumerate(range(0, m, part)):              # the same rows, shifted by one of eight offsets each time
+        e = min(m, r + part)
+        a[r:e], sa[r:e] = base[i % 8:i % 8 + e - r], scale[i % 8:i % 8 + e - r]
+    got = fp8q.int8_gemm(a, sa, b, sb, out_dtype=torch.bfloat16)
+    ref = (base.double() @ b.double().t()) * scale.double()[:, None] * sb.double()
+    tol = ref.abs() * (2.0 ** -8 + 8 * 2.0 ** -24) + 2.0 ** -100
+    for i, r in enumerate(range(0, m, part)):
+        e, o = min(m, r + part), i % 8
+        assert bool(((got[r:e].double() - ref[o:o + e - r]).abs() <= tol[o:o + e - r]).all()), r
+    del a, sa, got, ref, tol
+    torch.cuda.empty_cache()
