@@ -6,7 +6,7 @@ namespace fp8q {
 
 template <int OUT>
 static hipError_t go(const FfnArgs& p, hipStream_t st) {
-  return streams<true>(p) ? launch_stream<false, true, OUT>(p, st) : launch_tile<false, true, OUT>(p, st);
+  return streams(true, p.M, p.N) ? launch_stream<false, true, OUT>(p, st) : launch_tile<false, true, OUT>(p, st);
 }
 
 hipError_t launch_fp8_gated(const FfnArgs& p, bool out_bf16, hipStream_t st) {

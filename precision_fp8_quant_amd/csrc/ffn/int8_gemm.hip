@@ -6,7 +6,7 @@ namespace fp8q {
 
 template <bool GATED, int OUT>
 static hipError_t go(const FfnArgs& p, hipStream_t st) {
-  return streams<GATED>(p) ? launch_stream<true, GATED, OUT>(p, st) : launch_tile<true, GATED, OUT>(p, st);
+  return streams(GATED, p.M, p.N) ? launch_stream<true, GATED, OUT>(p, st) : launch_tile<true, GATED, OUT>(p, st);
 }
 
 hipError_t launch_int8_gemm(const FfnArgs& p, bool out_bf16, hipStream_t st) {

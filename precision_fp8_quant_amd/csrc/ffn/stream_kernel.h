@@ -285,60 +285,36 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(FfnArgs p) {
   }
 }
 
-template <bool INT8, bool GATED, int OUT, int MF, int NF, int WAVES, int UNROLL, bool HALF = false>
+template <bool INT8, bool GATED, int OUT, int I>
 static hipError_t launch_stream_cfg(const FfnArgs& p, hipStream_t st) {
-  return in_pieces(p, INT8, OUT == kOutBF16, 16 * MF, HALF ? 8 : 16 * NF, WAVES * 64, [&](const FfnArgs& q, unsigned grid) {
-    hipLaunchKernelGGL((stream_kernel<INT8, GATED, HALF, MF, NF, WAVES, UNROLL, OUT>), dim3(grid), dim3(WAVES * 64), 0, st,
-                       q);
+  constexpr StreamKernel S = kStreamKernels[I];
+  constexpr int UNROLL = S.mf == 1 && S.nf == 1 ? 4 : 2;
+  return in_pieces(p, INT8, OUT == kOutBF16, 16 * S.mf, S.half ? 8 : 16 * S.nf, S.waves * 64,
+                   [&](const FfnArgs& q, unsigned grid) {
+    hipLaunchKernelGGL((stream_kernel<INT8, GATED, S.half, S.mf, S.nf, S.waves, UNROLL, OUT>), dim3(grid),
+                       dim3(S.waves * 64), 0, st, q);
     return hipGetLastError();
   });
 }
 
-// Whether streaming beats the LDS tiles (tile_kernel.h).  Beyond 16 rows every
-// wave fetches as much of A beside its weight again, and streaming takes
-// (microseconds per 128-deep K-group and row of B) 3.5e-5 up to 32 rows and
-// 5.1e-5, but no less than 0.41 per group, up to 64; the tiles take 0.33 per
-// group with few rows of B, 0.44 with 7168, and 3e-5 per row with many.
-// Measured (us, streaming / tiles): 32 rows, 7168 rows of B by 18432 36 / 57,
-// 36864 by 7168 69 / 63, 4096 by 7168 16 / 17; 64 rows, the same 53 / 64,
-// 94 / 67, 23 / 18.5.
-template <bool GATED>
-static bool streams(const FfnArgs& p) {
-  const int64_t brows = GATED ? 2 * p.N : p.N;
-  return p.M <= 16 || (p.M <= 32 && brows <= 24000) || (p.M <= 64 && brows > 5500 && brows <= 8600);
-}
-
-// 16 waves where there are no more workgroups than CUs (FP8 gated 16x2048x7168
-// by 16 columns 12.2 us a call against 12.5), 8 otherwise (int8 1x7168x18432 26.0 against
-// 29.8).  Two column fragments per wave halve what a plain product fetches of A
-// (int8 16x7168x18432 29.0 against 36.8), if they leave enough workgroups; a
-// gated one has its two projections already (FP8 16x18432x7168 56.8 with one,
-// 58.9 with two).  Gated with at most 2048 columns, up to 32 rows: 8 columns a
-// workgroup, so that a CU streams half as much (us with 16 columns / with 8,
-// K = 7168: int8 1x2048 9.8 / 8.6, 16x2048 12.0 / 9.2, 32x2048 15.3 / 12.5,
-// 16x512 11.7 / 8.8; FP8 16x2048 12.1 / 9.9; with more columns than the CUs hold
-// at once it loses: int8 16x2688 12.1 / 16.1).  Eight of a plain product's
-// columns would leave half of each fragment empty, and gain nothing.
 template <bool INT8, bool GATED, int OUT>
 static hipError_t launch_stream(const FfnArgs& p, hipStream_t st) {
-  const bool few = (p.N + 15) / 16 <= 256;
+  const int i = stream_kernel_for(GATED, p.M, p.N);
   if constexpr (GATED) {
-    if ((p.N + 7) / 8 <= 256 && p.M <= 32)
-      return p.M <= 16 ? launch_stream_cfg<INT8, GATED, OUT, 1, 1, 16, 4, true>(p, st)
-                       : launch_stream_cfg<INT8, GATED, OUT, 2, 1, 16, 2, true>(p, st);
+    if (i == 0) return launch_stream_cfg<INT8, GATED, OUT, 0>(p, st);
+    if (i == 1) return launch_stream_cfg<INT8, GATED, OUT, 1>(p, st);
+  } else {
+    if (i == 2) return launch_stream_cfg<INT8, GATED, OUT, 2>(p, st);
+    if (i == 3) return launch_stream_cfg<INT8, GATED, OUT, 3>(p, st);
+    if (i == 4) return launch_stream_cfg<INT8, GATED, OUT, 4>(p, st);
   }
-  if constexpr (!GATED) {
-    if (p.M > 4 && (p.N + 31) / 32 >= 192) {
-      if (p.M <= 16) return launch_stream_cfg<INT8, GATED, OUT, 1, 2, 8, 2>(p, st);
-      if (p.M <= 32) return launch_stream_cfg<INT8, GATED, OUT, 2, 2, 8, 2>(p, st);
-      return launch_stream_cfg<INT8, GATED, OUT, 4, 2, 8, 2>(p, st);
-    }
+  switch (i) {
+    case 5: return launch_stream_cfg<INT8, GATED, OUT, 5>(p, st);
+    case 6: return launch_stream_cfg<INT8, GATED, OUT, 6>(p, st);
+    case 7: return launch_stream_cfg<INT8, GATED, OUT, 7>(p, st);
+    case 8: return launch_stream_cfg<INT8, GATED, OUT, 8>(p, st);
+    default: return launch_stream_cfg<INT8, GATED, OUT, 9>(p, st);
   }
-  if (p.M <= 16) return few ? launch_stream_cfg<INT8, GATED, OUT, 1, 1, 16, 4>(p, st)
-                            : launch_stream_cfg<INT8, GATED, OUT, 1, 1, 8, 4>(p, st);
-  if (p.M <= 32) return few ? launch_stream_cfg<INT8, GATED, OUT, 2, 1, 16, 2>(p, st)
-                            : launch_stream_cfg<INT8, GATED, OUT, 2, 1, 8, 2>(p, st);
-  return launch_stream_cfg<INT8, GATED, OUT, 4, 1, 8, 2>(p, st);
 }
 
 }  // namespace fp8q

@@ -410,98 +410,31 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
   }
 }
 
-template <bool INT8, bool GATED, int OUT, int BM, int BN, int WM, int PF, int STAGES, int KW>
+template <bool INT8, bool GATED, int OUT, int I>
 static hipError_t launch_tile_cfg(const FfnArgs& p, hipStream_t st) {
-  constexpr int THREADS = KW * WM * (BN / (32 * PF)) * 64;
-  return in_pieces(p, INT8, OUT == kOutBF16, BM, GATED ? BN / 2 : BN, THREADS, [&](const FfnArgs& q, unsigned grid) {
-    hipLaunchKernelGGL((tile_kernel<INT8, GATED, BM, BN, WM, PF, STAGES, KW, OUT>), dim3(grid), dim3(THREADS), 0, st, q);
+  constexpr Tiling T = kTilings[I];
+  constexpr int THREADS = T.kw * T.wm * (T.bn / (32 * T.pf)) * 64;
+  return in_pieces(p, INT8, OUT == kOutBF16, T.bm, GATED ? T.bn / 2 : T.bn, THREADS, [&](const FfnArgs& q, unsigned grid) {
+    hipLaunchKernelGGL((tile_kernel<INT8, GATED, T.bm, T.bn, T.wm, T.pf, 2, T.kw, OUT>), dim3(grid), dim3(THREADS), 0, st, q);
     return hipGetLastError();
   });
 }
 
 template <bool INT8, bool GATED, int OUT>
 static hipError_t launch_tile(const FfnArgs& p, hipStream_t st) {
-  // Five tilings (BM x BN by KW teams, waves of TM x 32 PF):
-  //   256x256x1  8 waves of 64x128, 1 workgroup per CU
-  //   128x128x1  4 waves of 64x64, 2
-  //   128x128x2  8 waves of 64x64, 1
-  //   64x64x2    8 waves of 16x64, 2
-  //   64x64x4    16 waves of 16x64, 1
-  // A larger tile reads fewer bytes per product, a smaller one spreads a small
-  // problem over more of the 256 CUs and rounds M and N up less; teams keep a CU
-  // busy that has one tile (more stages do not: a lone 64x64 tile took 35 us for
-  // 56 groups with 3 stages and with 6).  Measured microseconds per 128-deep
-  // K-group, for a CU's only tile, and per tile and CU when the CUs are full
-  // (int8, M = 80 .. 4096, K = 7168 and 18432; FP8 has the same ratios):
-  //   256x256x1 1.24  1.24    128x128x1 0.75  0.49    128x128x2 0.61  0.61
-  //   64x64x2   0.40  0.25    64x64x4   0.33  0.33
-  // A problem runs in rounds.  Where a CU holds one workgroup, each round of 256
-  // tiles, full or not, takes the one time per group.  Where it holds two, a
-  // round is 512 tiles and takes twice the second time; a last round takes the
-  // first time up to 256 tiles and a line between the two beyond.  The time is
-  // never less than the weight's 128 bytes a row take at the rate that each
-  // tiling was seen to stream a weight too large for the caches: 2.8, 3.3, 2.5,
-  // 2.5 and 2.8 TB/s.  To this comes what a round takes to fill and to leave,
-  // 7.4, 3.4, 2.5, 1.6 and 1.5 us, half of it where half a CU's tiles are left.
-  // The smallest wins.  Measured (us, in the order above):
-  //   int8  512x7168x7168   70  42  35  48  68
-  //   int8  128x7168x7168   68  43  35  23  19
-  //   int8 2048x7168x7168   80  96   -   -   -
-  //   int8 gated 64x18432x7168   -  67   -  80   -
-  //   int8 gated 128x18432x7168 94  81 107 107 126
-  //   FP8 gated 512x2048x7168   80  44  35  26  36
-  //   FP8 gated 1846x640x6016   70  38  32  41  47   (580 tiles of 64x64)
-  //   FP8 gated 4096x1408x2048  33  36  43  52  77
-  //   FP8 gated 2056x14976x640  73  65   - 131   -
-  //   int8  333x2000x512      10.7 5.8 6.5 4.5 5.1
-  //   int8 1024x4096x512      11.4 6.9 7.6 9.9 16.7
-  //   int8 4096x4096x512        15  17  27  35  64
-  const int64_t kg = (p.K + 127) / 128;
-  const auto cost = [&](int64_t n, int i) {        // microseconds for n of the N columns in tiling i
-    struct Tiling { int64_t bm, bn, kw; float alone, full, tbs, out; };
-    constexpr Tiling tilings[5] = {{256, 256, 1, 1.24f, 1.24f, 2.8f, 7.4f}, {128, 128, 1, 0.75f, 0.49f, 3.3f, 3.4f},
-                                   {128, 128, 2, 0.61f, 0.61f, 2.5f, 2.5f}, {64, 64, 2, 0.40f, 0.25f, 2.5f, 1.6f},
-                                   {64, 64, 4, 0.33f, 0.33f, 2.8f, 1.5f}};
-    const Tiling& s = tilings[i];
-    const int64_t cn = GATED ? s.bn / 2 : s.bn;
-    const int64_t tiles = ((p.M + s.bm - 1) / s.bm) * ((n + cn - 1) / cn), two = s.alone != s.full ? 2 : 1;
-    const int64_t last = tiles % (256 * two);
-    const float rounds = float(tiles / (256 * two));
-    const float beyond = last > 256 ? float(last - 256) / 256.0f : 0.0f;
-    const float c = rounds * float(two) * s.full + (last ? s.alone + beyond * (2 * s.full - s.alone) : 0.0f);
-    const float stream = float(n * (GATED ? 2 : 1)) * 128e-6f / s.tbs;
-    const float ends = rounds + (last > 256 || two == 1 ? float(last > 0) : last > 0 ? 0.5f : 0.0f);
-    return (c > stream ? c : stream) * float((kg + s.kw - 1) / s.kw * s.kw) + ends * s.out;
-  };
-  const auto pick = [&](int64_t n) {
-    int best = 0;
-    for (int i = 1; i < 5; ++i)
-      if (cost(n, i) < cost(n, best)) best = i;
-    return best;
-  };
-  const int best = pick(p.N);
-  // Whole columns of 256x256 tiles that fill rounds, and the other columns right
-  // behind them as a problem of their own in smaller tiles, where that is less
-  // by more than a launch (int8 8192x7168x18432, 3.5 rounds: 857 -> 820 us;
-  // int8 4200x4096x4096, 272 tiles: 85 -> 70; FP8 gated 2239x4608x3840: 100 -> 87).
-  constexpr int64_t CN = GATED ? 128 : 256;
-  const int64_t tm = (p.M + 255) / 256, tn = (p.N + CN - 1) / CN;
-  const int64_t whole = tm * tn / 256 * 256 / tm;  // such columns
-  if (whole > 0 && whole < tn) {
-    const int64_t cut = whole * CN;
-    if (cost(cut, 0) + cost(p.N - cut, pick(p.N - cut)) + 3.0f < cost(p.N, best)) {
-      const FfnArgs head = part_of(p, INT8, OUT == kOutBF16, 0, p.M, 0, cut);
-      const FfnArgs rest = part_of(p, INT8, OUT == kOutBF16, 0, p.M, cut, p.N - cut);
-      const hipError_t e = launch_tile_cfg<INT8, GATED, OUT, 256, 256, 4, 4, 2, 1>(head, st);
-      return e != hipSuccess ? e : launch_tile<INT8, GATED, OUT>(rest, st);
-    }
+  const TilePlan plan = tile_plan(GATED, p.M, p.N, p.K);
+  if (plan.cut) {
+    const FfnArgs head = part_of(p, INT8, OUT == kOutBF16, 0, p.M, 0, plan.cut);
+    const FfnArgs rest = part_of(p, INT8, OUT == kOutBF16, 0, p.M, plan.cut, p.N - plan.cut);
+    const hipError_t e = launch_tile_cfg<INT8, GATED, OUT, 0>(head, st);
+    return e != hipSuccess ? e : launch_tile<INT8, GATED, OUT>(rest, st);
   }
-  switch (best) {
-    case 0: return launch_tile_cfg<INT8, GATED, OUT, 256, 256, 4, 4, 2, 1>(p, st);
-    case 1: return launch_tile_cfg<INT8, GATED, OUT, 128, 128, 2, 2, 2, 1>(p, st);
-    case 2: return launch_tile_cfg<INT8, GATED, OUT, 128, 128, 2, 2, 2, 2>(p, st);
-    case 3: return launch_tile_cfg<INT8, GATED, OUT, 64, 64, 4, 2, 2, 2>(p, st);
-    default: return launch_tile_cfg<INT8, GATED, OUT, 64, 64, 4, 2, 2, 4>(p, st);
+  switch (plan.tiling) {
+    case 0: return launch_tile_cfg<INT8, GATED, OUT, 0>(p, st);
+    case 1: return launch_tile_cfg<INT8, GATED, OUT, 1>(p, st);
+    case 2: return launch_tile_cfg<INT8, GATED, OUT, 2>(p, st);
+    case 3: return launch_tile_cfg<INT8, GATED, OUT, 3>(p, st);
+    default: return launch_tile_cfg<INT8, GATED, OUT, 4>(p, st);
   }
 }
 

@@ -266,9 +266,8 @@ def test_fp8_gemm_gated_bf16(m, f, k):
     assert og.rel_frobenius(_f64(gu), og.round_bf16(ref)) <= 1e-3
 
 
-# Rows and columns for which each of the kernels' tilings and streaming variants is the one chosen: 256x256, 128x128 by
-# one team and 64x64 by two (128x128 by two and 64x64 by four on longer K, below); one, two and four row fragments, 16
-# waves, two column fragments; and a last round of 256x256 tiles that runs as a problem of its own.
+# Rows and columns on both sides of the limits between kernels.  Which size chooses which kernel, and a size for every
+# one of them: tests/ffn_kernel_sizes.py.
 VARIANTS = [(2040, 17348), (2000, 5300), (1300, 5000), (500, 7000), (500, 3000), (200, 1000), (3, 5000), (9, 6200), (30, 6200),
             (40, 6200), (30, 3000), (20, 8000), (60, 8000), (40, 3000)]
 
@@ -330,6 +329,7 @@ def test_fp8_gated_every_variant(m, f, k):
     gu_intact()
 
 
+# (Of these, 500 rows run in 128x128 tiles by two teams and 200 in 64x64 by two; four teams: tests/ffn_kernel_sizes.py.)
 @pytest.mark.parametrize("m, n", [(500, 7000), (200, 1000)])
 @pytest.mark.parametrize("gated", [False, True])
 def test_int8_teams_on_longer_k(m, n, gated):
