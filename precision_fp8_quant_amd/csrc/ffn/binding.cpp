@@ -89,6 +89,14 @@ PyObject* pair(const at::Tensor& a, const at::Tensor& b) {
   return t;
 }
 
+// Other threads run while a call allocates and launches: the allocator may wait
+// for another thread that holds its lock and wants the interpreter's, and a
+// launch for a full queue.  The caller's arguments stay referenced meanwhile.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 #define FP8Q_NONE_UNLESS(cond) \
   do {                         \
     if (!(cond)) Py_RETURN_NONE; \
@@ -108,12 +116,15 @@ PyObject* int8_gemm_call(PyObject*, PyObject* const* args, Py_ssize_t n) {
                    matrix(b, dev, &ldb) && a->size(1) == b->size(1) && whole_chunks(*a, lda) && whole_chunks(*b, ldb));
   const int64_t m = a->size(0), rows = b->size(0), k = a->size(1);
   FP8Q_NONE_UNLESS(floats(sa, dev, {m}) && floats(sb, dev, {rows}) && (!bias || floats(bias, dev, {rows})));
-  at::Tensor c = output(m, rows, out, dev, &ldc);
-  const int st = int8_gemm(m, rows, k, static_cast<const int8_t*>(a->data_ptr()), lda,
-                           static_cast<const float*>(sa->data_ptr()), static_cast<const int8_t*>(b->data_ptr()), ldb,
-                           static_cast<const float*>(sb->data_ptr()),
-                           bias ? static_cast<const float*>(bias->data_ptr()) : nullptr, c.data_ptr(), out, ldc,
-                           stream(dev));
+  at::Tensor c;
+  int st;
+  {
+    Unlocked others_run;
+    c = output(m, rows, out, dev, &ldc);
+    st = int8_gemm(m, rows, k, static_cast<const int8_t*>(a->data_ptr()), lda, static_cast<const float*>(sa->data_ptr()),
+                   static_cast<const int8_t*>(b->data_ptr()), ldb, static_cast<const float*>(sb->data_ptr()),
+                   bias ? static_cast<const float*>(bias->data_ptr()) : nullptr, c.data_ptr(), out, ldc, stream(dev));
+  }
   return answer(st, THPVariable_Wrap(c));
   END_HANDLE_TH_ERRORS
 }
@@ -131,10 +142,15 @@ PyObject* int8_gated_call(PyObject*, PyObject* const* args, Py_ssize_t n) {
                    matrix(b, dev, &ldb) && a->size(1) == b->size(1) && whole_chunks(*a, lda) && whole_chunks(*b, ldb));
   const int64_t m = a->size(0), rows = b->size(0), k = a->size(1);
   FP8Q_NONE_UNLESS(rows % 2 == 0 && floats(sa, dev, {m}) && floats(sb, dev, {rows}));
-  at::Tensor h = output(m, rows / 2, out, dev, &ldh);
-  const int st = int8_gemm_gated(act, m, rows / 2, k, static_cast<const int8_t*>(a->data_ptr()), lda,
-                                 static_cast<const float*>(sa->data_ptr()), static_cast<const int8_t*>(b->data_ptr()),
-                                 ldb, static_cast<const float*>(sb->data_ptr()), h.data_ptr(), out, ldh, stream(dev));
+  at::Tensor h;
+  int st;
+  {
+    Unlocked others_run;
+    h = output(m, rows / 2, out, dev, &ldh);
+    st = int8_gemm_gated(act, m, rows / 2, k, static_cast<const int8_t*>(a->data_ptr()), lda,
+                         static_cast<const float*>(sa->data_ptr()), static_cast<const int8_t*>(b->data_ptr()), ldb,
+                         static_cast<const float*>(sb->data_ptr()), h.data_ptr(), out, ldh, stream(dev));
+  }
   return answer(st, THPVariable_Wrap(h));
   END_HANDLE_TH_ERRORS
 }
@@ -149,13 +165,17 @@ PyObject* int8_quant_call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   int64_t ldx;
   FP8Q_NONE_UNLESS(matrix(x, dev, &ldx));
   const int64_t rows = x->size(0), cols = x->size(1), ldq = round_up(cols > 0 ? cols : 1, kChunk);
-  // the last row's bytes up to 16 exist too, as int8_gemm reads them
-  at::Tensor q = at::empty({rows, ldq}, at::TensorOptions().dtype(at::kChar).device(dev));
-  if (ldq != cols) q = q.as_strided({rows, cols}, {ldq, 1});
-  at::Tensor scales = at::empty({rows}, at::TensorOptions().dtype(at::kFloat).device(dev));
-  const int st = int8_quant_rows(x->data_ptr(), x->scalar_type() == at::kBFloat16 ? FP8Q_BF16 : FP8Q_F32, rows, cols,
-                                 ldx, static_cast<int8_t*>(q.data_ptr()), ldq, static_cast<float*>(scales.data_ptr()),
-                                 stream(dev));
+  at::Tensor q, scales;
+  int st;
+  {
+    Unlocked others_run;
+    // the last row's bytes up to 16 exist too, as int8_gemm reads them
+    q = at::empty({rows, ldq}, at::TensorOptions().dtype(at::kChar).device(dev));
+    if (ldq != cols) q = q.as_strided({rows, cols}, {ldq, 1});
+    scales = at::empty({rows}, at::TensorOptions().dtype(at::kFloat).device(dev));
+    st = int8_quant_rows(x->data_ptr(), x->scalar_type() == at::kBFloat16 ? FP8Q_BF16 : FP8Q_F32, rows, cols, ldx,
+                         static_cast<int8_t*>(q.data_ptr()), ldq, static_cast<float*>(scales.data_ptr()), stream(dev));
+  }
   return answer(st, pair(q, scales));
   END_HANDLE_TH_ERRORS
 }
@@ -174,12 +194,17 @@ PyObject* fp8_gated_call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   FP8Q_NONE_UNLESS(matrix(a, dev, &lda) && matrix(b, dev, &ldb) && a->size(1) == b->size(1));
   const int64_t m = a->size(0), rows = b->size(0), k = a->size(1), kg = (k + 127) / 128;
   FP8Q_NONE_UNLESS(rows % 2 == 0 && floats(sa, dev, {kg, m}) && floats(sb, dev, {(rows + 127) / 128, kg}));
-  at::Tensor h = output(m, rows / 2, out, dev, &ldh), gu;
-  if (keep) gu = output(m, rows, out, dev, &ldgu);
-  const int st = fp8_gemm_gated(act, m, rows / 2, k, static_cast<const uint8_t*>(a->data_ptr()), lda,
-                                static_cast<const float*>(sa->data_ptr()), static_cast<const uint8_t*>(b->data_ptr()),
-                                ldb, static_cast<const float*>(sb->data_ptr()), h.data_ptr(), out, ldh,
-                                keep ? gu.data_ptr() : nullptr, ldgu, stream(dev));
+  at::Tensor h, gu;
+  int st;
+  {
+    Unlocked others_run;
+    h = output(m, rows / 2, out, dev, &ldh);
+    if (keep) gu = output(m, rows, out, dev, &ldgu);
+    st = fp8_gemm_gated(act, m, rows / 2, k, static_cast<const uint8_t*>(a->data_ptr()), lda,
+                        static_cast<const float*>(sa->data_ptr()), static_cast<const uint8_t*>(b->data_ptr()), ldb,
+                        static_cast<const float*>(sb->data_ptr()), h.data_ptr(), out, ldh,
+                        keep ? gu.data_ptr() : nullptr, ldgu, stream(dev));
+  }
   return answer(st, keep ? pair(h, gu) : THPVariable_Wrap(h));
   END_HANDLE_TH_ERRORS
 }
@@ -199,13 +224,20 @@ PyObject* gated_backward_call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   FP8Q_NONE_UNLESS(gu->size(0) == m && gu->size(1) == f2 && f % 128 == 0);
   const auto bytes = at::TensorOptions().dtype(at::kByte).device(dev);
   const auto reals = at::TensorOptions().dtype(at::kFloat).device(dev);
-  at::Tensor q = at::empty({mp, f2}, bytes), s = at::empty({f2 / 128, mp}, reals);
-  at::Tensor qt = at::empty({f2, mp}, bytes), st = at::empty({mp / 128, f2}, reals);
-  const int status = fp8_gated_backward(
-      act, m, f, dh->data_ptr(), ld_dh, gu->data_ptr(), ld_gu,
-      dh->scalar_type() == at::kBFloat16 ? FP8Q_BF16 : FP8Q_F32, mode, static_cast<uint8_t*>(q.data_ptr()), f2,
-      static_cast<float*>(s.data_ptr()), static_cast<uint8_t*>(qt.data_ptr()), mp > 0 ? mp : 16,
-      static_cast<float*>(st.data_ptr()), nullptr, 0, stream(dev));
+  at::Tensor q, s, qt, st;
+  int status;
+  {
+    Unlocked others_run;
+    q = at::empty({mp, f2}, bytes);
+    s = at::empty({f2 / 128, mp}, reals);
+    qt = at::empty({f2, mp}, bytes);
+    st = at::empty({mp / 128, f2}, reals);
+    status = fp8_gated_backward(
+        act, m, f, dh->data_ptr(), ld_dh, gu->data_ptr(), ld_gu,
+        dh->scalar_type() == at::kBFloat16 ? FP8Q_BF16 : FP8Q_F32, mode, static_cast<uint8_t*>(q.data_ptr()), f2,
+        static_cast<float*>(s.data_ptr()), static_cast<uint8_t*>(qt.data_ptr()), mp > 0 ? mp : 16,
+        static_cast<float*>(st.data_ptr()), nullptr, 0, stream(dev));
+  }
   if (status != FP8Q_OK) return PyLong_FromLong(status);
   PyObject* t = PyTuple_New(4);
   if (!t) return nullptr;
