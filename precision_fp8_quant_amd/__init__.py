@@ -105,11 +105,12 @@ def _handle(stream, dev):
 _AS_IT_IS = contextlib.nullcontext()
 
 
-def _outputs_on(stream, dev):
-    """Context in which the outputs of a call on `stream` are allocated.  torch's allocator hands a freed block out
-    again in the order of the stream that it was allocated on: an output that was allocated on the current stream
-    and is written on another one could still be in use there, or be handed out while the kernel writes it."""
-    if stream is None:
+def _outputs_on(stream, dev, *outputs):
+    """Context in which those of a call's `outputs` that are None are allocated, for a call on `stream`.  torch's
+    allocator hands a freed block out again in the order of the stream that it was allocated on: an output that was
+    allocated on the current stream and is written on another one could still be in use there, or be handed out while
+    the kernel writes it."""
+    if stream is None or all(t is not None for t in outputs):
         return _AS_IT_IS
     handle = _handle(stream, dev)
     if handle == torch._C._cuda_getCurrentRawStream(dev.index):
@@ -195,7 +196,7 @@ def fp8_quant_tile(x, tile=TILE_1x128, mode=MAXABS, q=None, scales=None, stream=
     rows, cols = x.shape
     q_shape = (rows, cols) if tile == TILE_1x128 else (cols, rows)
     s_shape = (_cdiv(cols, 128), rows) if tile == TILE_1x128 else (_cdiv(rows, 128), cols)
-    with _outputs_on(stream, x.device):
+    with _outputs_on(stream, x.device, q, scales):
         if q is None:
             q = torch.empty(q_shape, dtype=torch.uint8, device=x.device)
         if scales is None:
@@ -213,7 +214,7 @@ def fp8_quant_tile_dual(x, mode=MAXABS, q=None, scales=None, q_t=None, scales_t=
     _rowmajor(x, "x")
     rows, cols = x.shape
     dev = x.device
-    with _outputs_on(stream, dev):
+    with _outputs_on(stream, dev, q, scales, q_t, scales_t):
         if q is None:
             q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
         if scales is None:
@@ -240,7 +241,7 @@ def fp8_quant_block(w, mode=MAXABS, transposed=False, q=None, scales=None, q_t=N
     dev = w.device
     if not transposed and (q_t is not None or scales_t is not None):
         raise ValueError("q_t / scales_t are the transposed copy: pass transposed=True")
-    with _outputs_on(stream, dev):
+    with _outputs_on(stream, dev, q, scales, *((q_t, scales_t) if transposed else ())):
         if q is None:
             q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
         if scales is None:
@@ -293,7 +294,7 @@ def _gemm(fn, kind, a, a_scales, b, b_scales, out_dtype, c, accumulate, stream, 
         sb_shape = (_cdiv(k, 128), n) if kind == WGRAD else (_cdiv(n, 128), _cdiv(k, 128))
         _expect(b_scales, "b_scales", torch.float32, sb_shape, dev, dense=True)
     if c is None:
-        with _outputs_on(stream, dev):
+        with _outputs_on(stream, dev, c):
             c = torch.empty((m, n), dtype=out_dtype, device=dev)
     if c.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"c must be bfloat16 or float32, got {c.dtype}")
@@ -321,7 +322,7 @@ def fp8_gemm_blockscaled_grouped(group_of_mtile, a, a_scales, b, b_scales, out_d
     _expect(a_scales, "a_scales", torch.float32, (_cdiv(k, 128), m), dev, dense=True)
     _expect(b_scales, "b_scales", torch.float32, (g, _cdiv(n, 128), _cdiv(k, 128)), dev, dense=True)
     if c is None:
-        with _outputs_on(stream, dev):
+        with _outputs_on(stream, dev, c):
             c = torch.empty((m, n), dtype=out_dtype, device=dev)
     if c.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"c must be bfloat16 or float32, got {c.dtype}")
@@ -338,7 +339,7 @@ def fp8_requant_1x128_to_128x1(q, scales, mode=POW2, q_t=None, scales_t=None, st
     rows, cols = q.shape
     dev = q.device
     _expect(scales, "scales", torch.float32, (_cdiv(cols, 128), rows), dev, dense=True)
-    with _outputs_on(stream, dev):
+    with _outputs_on(stream, dev, q_t, scales_t):
         if q_t is None:
             q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev)
         if scales_t is None:

@@ -101,8 +101,8 @@ def _dense(t, name, shape, device):
     return t.data_ptr()
 
 
-def _out(t, name, dtype, rows, cols, device, stream):
-    """The caller's output tensor, checked, or a new one on `stream`; its dtype code and leading dimension."""
+def _out(t, name, dtype, rows, cols, device):
+    """The caller's output tensor, checked, or a new one; its dtype code and leading dimension."""
     if t is not None:
         dtype = t.dtype
     code = _CODE.get(dtype)
@@ -112,10 +112,9 @@ def _out(t, name, dtype, rows, cols, device, stream):
         _expect(t, name, dtype, (rows, cols), device)
         return t, code, _ld(t)
     pad = -cols % (8 if code == BF16 else 4)
-    with _outputs_on(stream, device):
-        if pad:                                    # rows a multiple of 16 bytes apart
-            return torch.empty_strided((rows, cols), (cols + pad, 1), dtype=dtype, device=device), code, cols + pad
-        return torch.empty(rows, cols, dtype=dtype, device=device), code, cols or 1
+    if pad:                                        # rows a multiple of 16 bytes apart
+        return torch.empty_strided((rows, cols), (cols + pad, 1), dtype=dtype, device=device), code, cols + pad
+    return torch.empty(rows, cols, dtype=dtype, device=device), code, cols or 1
 
 
 def _ints(t, name):
@@ -157,13 +156,14 @@ def fp8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bfloa
     f, kg = n2 // 2, _cdiv(k, 128)
     sa = _dense(a_scales, "a_scales", (kg, m), dev)
     sb = _dense(b_scales, "b_scales", (_cdiv(n2, 128), kg), dev)
-    h, code, ldh = _out(h, "h", out_dtype, m, f, dev, stream)
     gu_ptr, ldgu = None, 0
-    if gu is not None or save_gate_up:
-        gu, gu_code, ldgu = _out(gu, "gu", h.dtype, m, n2, dev, stream)
-        if gu_code != code:
-            raise TypeError(f"gu must be {h.dtype} like h, got {gu.dtype}")
-        gu_ptr = gu.data_ptr()
+    with _outputs_on(stream, dev, h, gu if save_gate_up else h):
+        h, code, ldh = _out(h, "h", out_dtype, m, f, dev)
+        if gu is not None or save_gate_up:
+            gu, gu_code, ldgu = _out(gu, "gu", h.dtype, m, n2, dev)
+            if gu_code != code:
+                raise TypeError(f"gu must be {h.dtype} like h, got {gu.dtype}")
+            gu_ptr = gu.data_ptr()
     _call(lib.fp8_gemm_gated, dev, stream, act, m, f, k, a.data_ptr(), _ld(a), sa, b.data_ptr(), _ld(b), sb,
           h.data_ptr(), code, ldh, gu_ptr, ldgu)
     return h if gu is None else (h, gu)
@@ -187,7 +187,7 @@ def fp8_gated_backward(dh, gu, act=ACT_SILU, mode=MAXABS, q=None, scales=None, q
     mp, f2 = m + -m % 128, 2 * f
     _expect(gu, "gu", dtype, (m, f2), dev)
     ds, ts = (f2 // 128, mp), (mp // 128, f2)      # F is a multiple of 128 or the ABI's FP8Q_ERR_UNSUPPORTED
-    with _outputs_on(stream, dev):
+    with _outputs_on(stream, dev, q, scales, q_t, scales_t):
         if q is None:
             q = torch.empty(mp, f2, dtype=torch.uint8, device=dev)
         if scales is None:
@@ -219,7 +219,7 @@ def int8_quant_rows(x, q=None, scales=None, stream=None):
     code = _CODE.get(x.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {x.dtype} (bfloat16 or float32)")
-    with _outputs_on(stream, dev):
+    with _outputs_on(stream, dev, q, scales):
         if q is None:
             ld = max(cols + -cols % 16, 16)        # the last row's bytes up to 16 exist too, as int8_gemm reads them
             q = torch.empty(rows, ld, dtype=_i8, device=dev)
@@ -249,7 +249,8 @@ def int8_gemm(a, a_scales, b, b_scales, bias=None, out_dtype=torch.bfloat16, c=N
         raise ValueError(f"b must be a tensor on {dev}")
     sa, sb = _dense(a_scales, "a_scales", (m,), dev), _dense(b_scales, "b_scales", (n,), dev)
     bias_ptr = None if bias is None else _dense(bias, "bias", (n,), dev)
-    c, code, ldc = _out(c, "c", out_dtype, m, n, dev, stream)
+    with _outputs_on(stream, dev, c):
+        c, code, ldc = _out(c, "c", out_dtype, m, n, dev)
     _call(lib.int8_gemm, dev, stream, m, n, k, a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, bias_ptr, c.data_ptr(),
           code, ldc)
     return c
@@ -271,7 +272,8 @@ def int8_gemm_gated(a, a_scales, b, b_scales, act=ACT_SILU, out_dtype=torch.bflo
     if b.device != dev:
         raise ValueError(f"b must be a tensor on {dev}")
     sa, sb = _dense(a_scales, "a_scales", (m,), dev), _dense(b_scales, "b_scales", (n2,), dev)
-    h, code, ldh = _out(h, "h", out_dtype, m, n2 // 2, dev, stream)
+    with _outputs_on(stream, dev, h):
+        h, code, ldh = _out(h, "h", out_dtype, m, n2 // 2, dev)
     _call(lib.int8_gemm_gated, dev, stream, act, m, n2 // 2, k, a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb,
           h.data_ptr(), code, ldh)
     return h

@@ -71,6 +71,29 @@ def test_new_outputs_belong_to_the_given_stream(name, form):
     assert all(torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)) for a, b in zip(got, want))
 
 
+def test_given_outputs_leave_the_current_stream_alone(monkeypatch):
+    """Where nothing is allocated, a call on another stream does not change the current one on the way."""
+    fp8q = require_gpu()
+    x, w = torch.randn(256, 384, device="cuda", dtype=BF), torch.randn(512, 384, device="cuda", dtype=BF)
+    args = dict(zip("q scales q_t scales_t".split(), fp8q.fp8_quant_tile_dual(x)))
+    qw, sw = fp8q.fp8_quant_block(w)
+    h, gu = fp8q.fp8_gemm_gated(args["q"], args["scales"], qw, sw, save_gate_up=True)
+    back = dict(zip("q scales q_t scales_t".split(), fp8q.fp8_gated_backward(h, gu)))
+    want = [t.clone() for t in (h, gu, *back.values())]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    monkeypatch.setattr(torch.cuda, "stream", None)
+    fp8q.fp8_quant_tile_dual(x, **args, stream=s)
+    fp8q.fp8_gemm_gated(args["q"], args["scales"], qw, sw, h=h, gu=gu, stream=s)
+    fp8q.fp8_gated_backward(h, gu, **back, stream=s)
+    q, sq = torch.empty(256, 384, device="cuda", dtype=I8), torch.empty(256, device="cuda")
+    fp8q.int8_quant_rows(x, q=q, scales=sq, stream=s)
+    fp8q.int8_gemm(q, sq, q, sq, c=torch.empty(256, 256, device="cuda"), stream=s)
+    fp8q.int8_gemm_gated(q, sq, q, sq, h=torch.empty(256, 128, device="cuda"), stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((h, gu, *back.values()), want))
+
+
 def test_default_stream_by_handle():
     """The NULL handle from inside another stream's context: outputs and kernel on the default stream."""
     fp8q = require_gpu()
