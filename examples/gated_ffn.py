@@ -1,11 +1,11 @@
 """A gated feed-forward block, y = (silu(x Wg^T) * (x Wu^T)) Wd^T, trained in block-scaled FP8 and served in 8-bit
-integers:
+integers or in FP8:
 
     python examples/gated_ffn.py
 
 A block with random weights learns to imitate another one.  Every product of the training step and every quantization
 runs in the library's kernels; torch holds the master weights, the loss and the update.  The trained block then answers
-single tokens and a batch with 8-bit weights and activations.
+single tokens and a batch with 8-bit weights and activations, integers or FP8.
 """
 
 import os
@@ -57,6 +57,10 @@ class GatedFFN:
         """8-bit codes of both weights with one scale for each output channel."""
         return (*fp8q.int8_quant_rows(self.w_gu), *fp8q.int8_quant_rows(self.w_d))
 
+    def for_serving_fp8(self):
+        """FP8 codes of both weights with one scale for each 128x128 block."""
+        return (*fp8q.fp8_quant_block(self.w_gu), *fp8q.fp8_quant_block(self.w_d))
+
 
 def serve(weights, x):
     """The block on any number of tokens, one included, in 8-bit integers."""
@@ -64,6 +68,18 @@ def serve(weights, x):
     qx, sx = fp8q.int8_quant_rows(x)
     qh, sh = fp8q.int8_quant_rows(fp8q.int8_gemm_gated(qx, sx, qw, sw))
     return fp8q.int8_gemm(qh, sh, qd, sd)
+
+
+def serve_fp8(weights, x):
+    """The block on any number of tokens, one included, in block-scaled FP8.  The down projection takes rows in whole
+    tiles of 128: h is the head of a buffer of such tiles, whose other rows are zeros."""
+    qw, sw, qd, sd = weights
+    n = x.shape[0]
+    qx, sx = fp8q.fp8_quant_tile(x)
+    h = torch.zeros((n + -n % 128, qd.shape[1]), dtype=torch.bfloat16, device=x.device)
+    fp8q.fp8_gemm_gated(qx, sx, qw, sw, h=h[:n])
+    qh, sh = fp8q.fp8_quant_tile(h)
+    return fp8q.fp8_gemm_blockscaled(fp8q.FPROP, qh, sh, qd, sd)[:n]
 
 
 def train(block, teacher, steps, tokens, lr=0.02, seed=0, log=None):
@@ -92,11 +108,11 @@ def main():
     teacher, block = GatedFFN(d, f, seed=1), GatedFFN(d, f, seed=2)
     losses = train(block, teacher, steps=400, tokens=tokens, lr=0.1, log=print)
     print(f"loss {losses[0]:.5f} -> {losses[-1]:.5f}")
-    weights = block.for_serving()
-    for n in (1, 17, 300):
-        x = torch.randn((n, d), device="cuda", dtype=torch.bfloat16)
-        y, ref = serve(weights, x).float(), block.reference(x)
-        print(f"served {n:3d} tokens in 8-bit integers: relative error {(y - ref).norm() / ref.norm():.4f}")
+    for form, answer, weights in (("8-bit integers", serve, block.for_serving()), ("FP8", serve_fp8, block.for_serving_fp8())):
+        for n in (1, 17, 300):
+            x = torch.randn((n, d), device="cuda", dtype=torch.bfloat16)
+            y, ref = answer(weights, x).float(), block.reference(x)
+            print(f"served {n:3d} tokens in {form}: relative error {(y - ref).norm() / ref.norm():.4f}")
 
 
 if __name__ == "__main__":

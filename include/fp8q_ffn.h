@@ -6,7 +6,10 @@
  *
  * is trained in block-scaled FP8 (fp8_gemm_gated, fp8_gated_backward around
  * the quantizers and GEMMs of fp8q.h) and served in FP8 or in 8-bit integers
- * (int8_quant_rows, int8_gemm, int8_gemm_gated).
+ * (int8_quant_rows, int8_gemm, int8_gemm_gated).  The operators here take any
+ * number of tokens; fp8_gemm_blockscaled, which does the down projection in
+ * FP8, takes rows in whole tiles of 128: let h be the head of a buffer of such
+ * tiles whose other rows are zeros, and quantize and multiply the buffer.
  *
  * Every convention of fp8q.h holds here: device pointers owned by the caller,
  * no allocation, no state, no synchronisation, all work on `stream`, plain int
@@ -41,7 +44,10 @@ typedef enum { FP8Q_ACT_SILU = 0, FP8Q_ACT_GELU_TANH = 1 } fp8q_act;
  *   g[m][f] = sum_k A[m][k] B[f][k],  u[m][f] = sum_k A[m][k] B[F+f][k]
  *   h[m][f] = act(g[m][f]) * u[m][f]
  * with the per-128-K-group scales and FP32 promotion of fp8_gemm_blockscaled
- * (FPROP).
+ * (FPROP), and its precision: within a K-group the matrix instruction drops
+ * low bits of its partial sums, so that g and u are off by about 1.5e-5 (5e-5
+ * where codes fill their range) in relative Frobenius terms -- more than the
+ * rounding of an FP32 output, less than that of a BF16 one.
  *
  * a        : A[M][K] E4M3, leading dimension lda (bytes); any M, one token included.
  * a_scales : [K/128][M] packed (fp8_quant_tile, FP8Q_TILE_1x128).
