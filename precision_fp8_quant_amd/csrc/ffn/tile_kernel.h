@@ -36,7 +36,7 @@ namespace fp8q {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 
-template <bool INT8, bool GATED, int BM, int BN, int WM, int PF, int STAGES, int KW, int OUT>
+template <bool INT8, bool GATED, int BM, int BN, int WM, int PF, int KW, int OUT>
 __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(FfnArgs p) {
   constexpr int WN = BN / (32 * PF);    // waves along B's rows
   constexpr int NW = WM * WN;           // waves per team; KW teams take the K-groups in turn
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
   static_assert(INT8 || (128 % CN == 0 && BM / 64 <= NW), "FP8: a tile in one scale block, one A-scale DMA a wave");
   constexpr int ESZ = OUT == kOutBF16 ? 2 : 4;
   constexpr int PITCH = PC * ESZ + 16;           // bytes per staged output row
-  constexpr int LOOP_LDS = KW * STAGES * STAGE;
+  constexpr int LOOP_LDS = KW * 2 * STAGE;
   constexpr int EPI_LDS = NW * TM * PITCH;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[LOOP_LDS > EPI_LDS ? LOOP_LDS : EPI_LDS];
 
@@ -63,7 +63,7 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
   const int team = KW > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / NW : 0;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) - team * NW;     // within the team
   const int tid = threadIdx.x - team * (NW * 64);
-  uint8_t* const smem = lds + team * (STAGES * STAGE);
+  uint8_t* const smem = lds + team * (2 * STAGE);
   const int wm = wave / WN, wn = wave % WN;
   const int lr = lane & 15, lq = lane >> 4;
 
@@ -165,37 +165,31 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
 #pragma unroll
       for (int c = 0; c < PF; ++c) acc[a][b][c] = acc_t{0, 0, 0, 0};
 
-  // Team `team` computes groups team, team + KW, ... in its own ring of stages
-  // (below, "group g" is a team's g-th).  Groups 0 .. STAGES-2 are under way
-  // before the loop, group g + STAGES-1 is requested while group g is computed,
-  // into the stage that group g-1 has left.
-  // Loads return in order, so a wave's part of group g has landed once at most
-  // the STAGES-2 younger groups' DMAs are outstanding; the barrier then says so
-  // for every wave, and that every wave is done with group g-1.  Past the last
-  // group the last one is requested again, which keeps the count; its copies
-  // land in stages that are not read any more, before the epilogue's barrier.
-  constexpr int YOUNGER = (STAGES - 2) * (A_DMA + B_DMA);
-  static_assert(STAGES >= 2 && YOUNGER < 64, "vmcnt holds six bits");
+  // Team `team` computes groups team, team + KW, ... in two stages of its own
+  // (below, "group g" is a team's g-th).  Group 0 is under way before the loop,
+  // group g + 1 is requested while group g is computed, into the stage that
+  // group g-1 has left.
+  // A wave's part of group g has landed once none of its DMAs is outstanding;
+  // the barrier then says so for every wave, and that every wave is done with
+  // group g-1.  Past the last group the last one is requested again; its copy
+  // lands in the stage that is not read any more, before the epilogue's barrier.
   auto clampg = [&](int64_t i) {                  // K-group of this team's i-th turn
     const int64_t g = i * KW + team;
     return g < KG ? g : KG - 1;
   };
   const int64_t turns = (KG + KW - 1) / KW;
   if (KG > 0) {
+    issue_scales(clampg(0), 0);
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-      issue_scales(clampg(s), s);
-#pragma unroll
-      for (int i = 0; i < A_DMA + B_DMA; ++i) issue_dma(clampg(s), s, i);
-    }
+    for (int i = 0; i < A_DMA + B_DMA; ++i) issue_dma(clampg(0), 0, i);
   }
 
   int stage = 0;
   for (int64_t g = 0; g < turns; ++g) {
-    __builtin_amdgcn_s_waitcnt(0x0F70 | (YOUNGER & 15) | ((YOUNGER >> 4) << 14));    // vmcnt(YOUNGER)
+    wait_vmem_all();
     __syncthreads();
-    const int64_t gn = clampg(g + STAGES - 1);
-    const int stage_n = stage == 0 ? STAGES - 1 : stage - 1;
+    const int64_t gn = clampg(g + 1);
+    const int stage_n = stage ^ 1;
     issue_scales(gn, stage_n);
     uint8_t* const ta = smem + stage * STAGE;
     const uint8_t* const tb = ta + A_BYTES;
@@ -268,7 +262,7 @@ __global__ __launch_bounds__(KW * WM * (BN / (32 * PF)) * 64) void tile_kernel(F
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    stage ^= 1;
   }
   wait_vmem_all();                               // what follows reuses the stages
   __syncthreads();
@@ -415,7 +409,7 @@ static hipError_t launch_tile_cfg(const FfnArgs& p, hipStream_t st) {
   constexpr Tiling T = kTilings[I];
   constexpr int THREADS = T.kw * T.wm * (T.bn / (32 * T.pf)) * 64;
   return in_pieces(p, INT8, OUT == kOutBF16, T.bm, GATED ? T.bn / 2 : T.bn, THREADS, [&](const FfnArgs& q, unsigned grid) {
-    hipLaunchKernelGGL((tile_kernel<INT8, GATED, T.bm, T.bn, T.wm, T.pf, 2, T.kw, OUT>), dim3(grid), dim3(THREADS), 0, st, q);
+    hipLaunchKernelGGL((tile_kernel<INT8, GATED, T.bm, T.bn, T.wm, T.pf, T.kw, OUT>), dim3(grid), dim3(THREADS), 0, st, q);
     return hipGetLastError();
   });
 }
