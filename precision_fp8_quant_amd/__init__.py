@@ -124,7 +124,7 @@ def _run(fn, dev, stream, *args):
     """Call entry point `fn` with the tensors' device `dev` current and the stream resolved on it: the kernels run
     on the stream's device, and the NULL stream (torch's default stream) is the current device's.  Where `dev` is
     current already, as it nearly always is, no device guard is set up and the current stream's handle is asked for
-    directly: a small int8_gemm call took 15.8 us and takes 9.5, of which the launch is 3."""
+    directly, which saves a call 6 us (a small fp8_quant_tile call takes 11)."""
     handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _handle(stream, dev)
     if torch._C._cuda_getDevice() == dev.index:
         status = fn(*args, handle)

@@ -2,8 +2,8 @@
 // step: new outputs, the current stream of the current device.  Tensors are
 // checked, outputs allocated and the C ABI (include/fp8q_ffn.h) called without
 // an interpreted line in between, because a caller with few tokens waits for
-// the host: from Python a small int8_gemm call takes 8.1 us, of which the
-// launch itself is 3.
+// the host: a small int8_gemm call takes 4.5 us, of which the launch itself is
+// 3, and 8.2 through ctypes.
 //
 // A function here answers None when anything is not as it expects; ffn.py then
 // takes the call its own way, with the message that says what is wrong.  It

@@ -97,7 +97,7 @@ constexpr Tiling kTilings[] = {{256, 256, 1, 4, 4, 1.24f, 1.24f, 2.8f, 7.4f},
 // Microseconds for an M x N product in tiling i.  A larger tile reads fewer
 // bytes per product, a smaller one spreads a small problem over more of the 256
 // CUs and rounds M and N up less; teams keep a CU busy that has one tile (more
-// stages do not: a lone 64x64 tile took 35 us for 56 groups with 3 stages and
+// than two stages do not: a lone 64x64 tile took 35 us for 56 groups with 3 and
 // with 6).  Measured microseconds per 128-deep K-group, for a CU's only tile
 // (alone), and per tile and CU when the CUs are full (int8, M = 80 .. 4096,
 // K = 7168 and 18432; FP8 has the same ratios): the first two columns above.
