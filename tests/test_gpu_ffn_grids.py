@@ -85,3 +85,31 @@ def test_int8_product_of_more_rows_than_one_launch_takes():
         assert bool(((got[r:e].double() - ref[o:o + e - r]).abs() <= tol[o:o + e - r]).all()), r
     del a, sa, got, ref, tol
     torch.cuda.empty_cache()
+
+
+def test_fp8_gemm_gated_of_more_columns_than_one_launch_takes():
+    """2^27 + 128 columns, 128 deep: the second launch has its own weight scales and its own columns of h and of g and u.
+    The weight is one block of rows again and again, with other scales each time."""
+    fp8q = require_gpu()
+    m, f, k, part = 2, (1 << 27) + 128, 128, 1 << 20
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    qa, sa = fp8q.fp8_quant_tile(torch.randn((m, k), generator=gen, device="cuda"))
+    base, _ = fp8q.fp8_quant_block(torch.randn((part, k), generator=gen, device="cuda") * 0.1)
+    qb = torch.empty((2 * f, k), dtype=torch.uint8, device="cuda")
+    for r in range(0, 2 * f, part):
+        qb[r:r + part] = base[:min(part, 2 * f - r)]
+    sb = torch.rand((2 * f // 128, 1), generator=gen, device="cuda") * 1e-3 + 1e-4
+    h, gu = fp8q.fp8_gemm_gated(qa, sa, qb, sb, out_dtype=torch.float32, save_gate_up=True)
+    dots = (qa.view(torch.float8_e4m3fn).double() * sa.double().t()) @ base.view(torch.float8_e4m3fn).double().t()
+    for r in range(0, 2 * f, part):
+        n = min(part, 2 * f - r)
+        ref = dots[:, :n] * sb[r // 128:(r + n) // 128].double().t().repeat_interleave(128, 1)
+        got = gu[:, r:r + n].double()
+        assert ((got - ref).norm() / ref.norm()).item() <= 2e-4, r         # the bound of the plain FP8 GEMMs
+    for c in range(0, f, 1 << 24):
+        g, u = gu[:, c:min(f, c + (1 << 24))].double(), gu[:, f + c:f + min(f, c + (1 << 24))].double()
+        ref = g * torch.sigmoid(g) * u
+        tol = (18 + 8 * g.abs()) * 2.0 ** -24 * ref.abs() + 2.0 ** -100 * (1 + (g * u).abs())
+        assert bool(((h[:, c:c + (1 << 24)].double() - ref).abs() <= tol).all()), c
+    del qb, h, gu
+    torch.cuda.empty_cache()
