@@ -1,4 +1,4 @@
-"""Python binding of the fp8q C ABI (include/fp8q.h, include/fp8q_ffn.h) for AMD MI355X.
+"""Python binding of the fp8q C ABI (include/fp8q.h, fp8q_ffn.h, fp8q_front.h) for AMD MI355X.
 
 Argument marshalling only: every step of quantization and GEMM runs in the
 HIP kernels of ``libfp8q.so``.  torch supplies device memory and the stream.
@@ -15,7 +15,9 @@ Functions keep the C names:
     fp8_gemm_blockscaled_grouped(gmap, a, sa, b, sb) -> c
     fp8_requant_1x128_to_128x1(q, scales, mode) -> (q_t, scales_t)
 and, from include/fp8q_ffn.h (module ``ffn``), the gated feed-forward operators fp8_gemm_gated, fp8_gated_backward,
-int8_quant_rows, int8_gemm and int8_gemm_gated.
+int8_quant_rows, int8_gemm and int8_gemm_gated;
+from include/fp8q_front.h (module ``front``), the operators in front of the projections fp8_rmsnorm, int8_rmsnorm,
+rmsnorm_backward, moe_route, moe_route_backward and fp8_moe_dispatch.
 FP8 tensors are torch.uint8 holding OCP E4M3FN codes.
 
 stream= takes a torch stream or a raw handle; without it a call goes to the current stream of the tensors' device.
@@ -353,3 +355,5 @@ def fp8_requant_1x128_to_128x1(q, scales, mode=POW2, q_t=None, scales_t=None, st
 
 from .ffn import (ACT_GELU_TANH, ACT_SILU, fp8_gated_backward, fp8_gemm_gated, int8_gemm,  # noqa: E402
                   int8_gemm_gated, int8_quant_rows)
+from .front import (fp8_moe_dispatch, fp8_rmsnorm, int8_rmsnorm, moe_max_rows, moe_route, moe_route_backward,  # noqa: E402
+                    rmsnorm_backward)

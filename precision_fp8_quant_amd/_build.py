@@ -18,8 +18,9 @@ LIB_PATH = os.path.join(PKG_DIR, "libfp8q.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 DEVICE_SOURCES = ["quant.hip", "gemm.hip", "gemm_pow2.hip", "ffn/fp8_gated.hip", "ffn/int8_gemm.hip",
-                  "ffn/int8_quant.hip", "ffn/gated_backward.hip"]
-HOST_SOURCES = ["abi.cpp", "ffn/abi_ffn.cpp"]
+                  "ffn/int8_quant.hip", "ffn/gated_backward.hip", "front/rmsnorm.hip", "front/rmsnorm_backward.hip",
+                  "front/route.hip", "front/dispatch.hip"]
+HOST_SOURCES = ["abi.cpp", "ffn/abi_ffn.cpp", "front/abi_front.cpp"]
 
 # -ffp-contract=off: the quantizer's scale-multiply-then-round sequence must be
 # exactly the stated FP32 operations (no fused multiply-add formed behind our

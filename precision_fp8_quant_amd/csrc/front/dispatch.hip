@@ -1,0 +1,267 @@
+// Rows of codes in the order of their experts, each expert's rows padded to
+// whole 128-row tiles.
+//
+//   s_e = 128 sum_{i<e} ceil(c_i / 128),  row(t, j) = s_e + slots of e before (t, j)
+// The order within an expert is the order of the slots (t k + j), so the result
+// does not depend on timing.  A wave takes a chunk of slots 64 at a time: lanes
+// of equal experts find each other by one ballot per bit of the expert, a
+// lane's place is the expert's running count plus its equals in lower lanes.
+//   up to 8192 slots   one workgroup: counts of its 16 waves' chunks, their
+//                      prefix sums and the tile map, the rows
+//   beyond             the three steps as kernels of their own, over up to 128
+//                      chunks
+// Then one kernel moves codes and scales: a token's row is read once and
+// written to its k places; scales, which lie transposed, are written in runs of
+// a tile's 128 rows, with the padding rows of the tile.
+#include "front_launch.h"
+#include "lanes.h"
+#include "row_io.h"
+
+namespace fp8q {
+namespace {
+
+constexpr uint32_t kZeroScaleBits = 0x00800000u;   // 2^-126: the scale of a row of zeros
+
+__device__ __forceinline__ int expert_at(const DispatchArgs& p, int64_t slot, int64_t end) {
+  if (slot >= end) return -1;
+  const int e = p.experts[slot];
+  return e >= 0 && e < int(p.E) ? e : -1;
+}
+
+// Adds the experts of slots [begin, end) to count[], by one wave.
+__device__ __forceinline__ void count_chunk(const DispatchArgs& p, int64_t begin, int64_t end, int* count) {
+  for (int64_t s = begin; s < end; s += 64) {
+    const int e = expert_at(p, s + (threadIdx.x & 63), end);
+    if (e >= 0) atomicAdd(&count[e], 1);           // integers: the order does not matter
+  }
+}
+
+// The rows of slots [begin, end), by one wave; next[e] is e's next row, in LDS
+// that no other wave writes.
+__device__ __forceinline__ void place_chunk(const DispatchArgs& p, int64_t begin, int64_t end, int bits, int* next) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t s = begin; s < end; s += 64) {      // uniform over the wave
+    const int64_t slot = s + lane;
+    const int e = expert_at(p, slot, end);
+    uint64_t same = __ballot(e >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t one = __ballot((e >> b) & 1);
+      same &= (e >> b) & 1 ? one : ~one;
+    }
+    const uint64_t below = (uint64_t(1) << lane) - 1;
+    int row = -1;
+    if (e >= 0) row = next[e] + __popcll(same & below);
+    asm volatile("" ::: "memory");                 // the wave's reads come before its writes (LDS keeps their order)
+    if (e >= 0 && (same & below) == 0) next[e] = row + __popcll(same);
+    asm volatile("" ::: "memory");
+    if (slot < end) p.row_of_slot[slot] = row;
+    if (e >= 0) p.token_of_row[row] = int32_t(slot / p.k);
+  }
+}
+
+// Exclusive sums over the workgroup's 1024 threads; *total is the sum.
+__device__ __forceinline__ int block_exclusive(int v, int* wave_sum, int* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int s = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(s, d, 64);
+    if (lane >= d) s += o;
+  }
+  if (lane == 63) wave_sum[wave] = s;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) {
+    before += w < wave ? wave_sum[w] : 0;
+    all += wave_sum[w];
+  }
+  *total = all;
+  return before + s - v;
+}
+
+// The tile map and the rows that hold no token, by 1024 threads: thread e < E
+// has expert e's count and first tile.
+__device__ __forceinline__ void write_maps(const DispatchArgs& p, int count, int first, int tiles_used, int (*place)[2]) {
+  const int t = threadIdx.x, tiles = int(p.M_total >> 7);
+  const int mine = (count + 127) >> 7;
+  if (t < int(p.E)) {
+    for (int i = 0; i < mine; ++i) p.group_of_mtile[first + i] = t;
+    place[t][0] = first * 128 + count;             // padding rows: [0] to [1]
+    place[t][1] = (first + mine) * 128;
+  }
+  for (int i = tiles_used + t; i < tiles; i += 1024) p.group_of_mtile[i] = -1;
+  for (int64_t i = int64_t(tiles_used) * 128 + t; i < p.M_total; i += 1024) p.token_of_row[i] = -1;
+  __syncthreads();
+  for (int i = t; i < int(p.E) * 128; i += 1024) {
+    const int row = place[i >> 7][0] + (i & 127);
+    if (row < place[i >> 7][1]) p.token_of_row[row] = -1;
+  }
+}
+
+__global__ __launch_bounds__(1024) void plan_kernel(DispatchArgs p, int chunk, int bits) {
+  __shared__ int next[16][kMaxExperts];
+  __shared__ int place[kMaxExperts][2];
+  __shared__ int wave_sum[16];
+  const int t = threadIdx.x, wave = t >> 6, E = int(p.E);
+  const int64_t slots = p.T * p.k, begin = int64_t(wave) * chunk;
+  const int64_t end = begin + chunk < slots ? begin + chunk : slots;
+  for (int i = t; i < 16 * E; i += 1024) next[i / E][i % E] = 0;
+  __syncthreads();
+  count_chunk(p, begin, end, next[wave]);
+  __syncthreads();
+  int count = 0;
+  if (t < E) {
+#pragma unroll
+    for (int w = 0; w < 16; ++w) count += next[w][t];
+  }
+  int used;
+  const int first = block_exclusive((count + 127) >> 7, wave_sum, &used);
+  if (t < E) {
+    int row = first * 128;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      const int c = next[w][t];
+      next[w][t] = row;
+      row += c;
+    }
+  }
+  write_maps(p, count, first, used, place);        // its barrier is also that of next[]
+  place_chunk(p, begin, end, bits, next[wave]);
+}
+
+__global__ __launch_bounds__(256) void plan_count_kernel(DispatchArgs p, int64_t chunk, int64_t chunks) {
+  __shared__ int count[4][kMaxExperts];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, E = int(p.E);
+  const int64_t c = int64_t(blockIdx.x) * 4 + wave;
+  for (int e = lane; e < E; e += 64) count[wave][e] = 0;
+  __syncthreads();
+  if (c < chunks) {
+    const int64_t slots = p.T * p.k, end = (c + 1) * chunk < slots ? (c + 1) * chunk : slots;
+    count_chunk(p, c * chunk, end, count[wave]);
+  }
+  __syncthreads();
+  if (c < chunks)
+    for (int e = lane; e < E; e += 64) p.hist[c * E + e] = count[wave][e];
+}
+
+// hist[c][e] becomes the first row of expert e's slots in chunk c.  Up to 16
+// threads (1024 over E rounded up to a power of two) take an expert's chunks in
+// consecutive pieces.
+__global__ __launch_bounds__(1024) void plan_scan_kernel(DispatchArgs p, int chunks, int log_e) {
+  __shared__ int sums[1024];
+  __shared__ int firsts[kMaxExperts];
+  __shared__ int place[kMaxExperts][2];
+  __shared__ int wave_sum[16];
+  const int t = threadIdx.x, E = int(p.E), ep = 1 << log_e, share = log_e < 6 ? 16 : 1024 >> log_e;
+  const int e = t & (ep - 1), piece = t >> log_e, len = (chunks + share - 1) / share;
+  const int c0 = piece * len, c1 = c0 + len < chunks ? c0 + len : chunks;
+  int sum = 0;
+  const bool busy = e < E && piece < share;
+  if (busy) {
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) sum += p.hist[int64_t(c) * E + e];
+  }
+  sums[t] = sum;
+  __syncthreads();
+  int count = 0;
+  if (t < E)
+    for (int s = 0; s < share; ++s) count += sums[s * ep + t];
+  int used;
+  const int first = block_exclusive((count + 127) >> 7, wave_sum, &used);
+  if (t < E) firsts[t] = first;
+  __syncthreads();
+  if (busy) {
+    int row = firsts[e] * 128;
+    for (int s = 0; s < piece; ++s) row += sums[s * ep + e];
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) {
+      const int n = p.hist[int64_t(c) * E + e];
+      p.hist[int64_t(c) * E + e] = row;
+      row += n;
+    }
+  }
+  write_maps(p, count, first, used, place);
+}
+
+__global__ __launch_bounds__(256) void plan_place_kernel(DispatchArgs p, int64_t chunk, int64_t chunks, int bits) {
+  __shared__ int next[4][kMaxExperts];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, E = int(p.E);
+  const int64_t c = int64_t(blockIdx.x) * 4 + wave;
+  if (c < chunks)
+    for (int e = lane; e < E; e += 64) next[wave][e] = p.hist[c * E + e];
+  __syncthreads();
+  if (c < chunks) {
+    const int64_t slots = p.T * p.k, end = (c + 1) * chunk < slots ? (c + 1) * chunk : slots;
+    place_chunk(p, c * chunk, end, bits, next[wave]);
+  }
+}
+
+// Work units: first every tile in pieces of 16 groups (2048 codes of a row),
+// then every token in pieces of 1024 codes, one wave each.
+__global__ __launch_bounds__(256) void move_kernel(DispatchArgs p, int64_t tile_units, int64_t blocks) {
+  __shared__ int token[128];
+  const int t = threadIdx.x;
+  const int64_t groups = p.D >> 7;
+  for (int64_t u = blockIdx.x; u < blocks; u += gridDim.x) {     // block-uniform: barriers stay matched
+    if (u < tile_units) {
+      const int64_t pieces = (groups + 15) >> 4, tile = u / pieces, g0 = u % pieces * 16;
+      if (p.group_of_mtile[tile] < 0) continue;
+      const int64_t g1 = g0 + 16 < groups ? g0 + 16 : groups;
+      const int mine = p.token_of_row[tile * 128 + (t & 127)];
+      __syncthreads();                             // token[] may still be read for the last tile
+      if (t < 128) token[t] = mine;
+      __syncthreads();
+      for (int64_t g = g0 + (t >> 7); g < g1; g += 2)
+        p.a_scales[g * p.M_total + tile * 128 + (t & 127)] =
+            mine >= 0 ? p.scales[g * p.T + mine] : __uint_as_float(kZeroScaleBits);
+      const int64_t col = g0 * 128 + (t & 127) * 16;
+      if (col < p.D)
+        for (int r = t >> 7; r < 128; r += 2)
+          if (token[r] < 0) *reinterpret_cast<u32x4*>(p.a + (tile * 128 + r) * p.ld_a + col) = u32x4{0u, 0u, 0u, 0u};
+    } else {
+      const int64_t pieces = (p.D + 1023) >> 10, w = (u - tile_units) * 4 + (t >> 6);
+      const int64_t tok = w / pieces, col = (w % pieces) * 1024 + (t & 63) * 16;
+      if (tok >= p.T || col >= p.D) continue;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p.q + tok * p.ld_q + col);
+      for (int j = 0; j < int(p.k); ++j) {
+        const int row = p.row_of_slot[tok * p.k + j];
+        if (row >= 0) *reinterpret_cast<u32x4*>(p.a + row * p.ld_a + col) = v;
+      }
+    }
+  }
+}
+
+int bits_of(int64_t E) {                           // bits that tell E experts apart
+  int b = 0;
+  while ((int64_t(1) << b) < E) ++b;
+  return b;
+}
+
+}  // namespace
+
+hipError_t launch_moe_dispatch(const DispatchArgs& p, hipStream_t st) {
+  const int64_t slots = p.T * p.k, chunks = dispatch_chunks(slots);
+  const int bits = bits_of(p.E);
+  if (chunks == 0) {
+    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(1024), 0, st, p, int((slots + 1023) / 1024 * 64), bits);
+  } else {
+    const int64_t chunk = dispatch_chunk(slots);
+    const dim3 grid(unsigned((chunks + 3) / 4));
+    hipLaunchKernelGGL(plan_count_kernel, grid, dim3(256), 0, st, p, chunk, chunks);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(plan_scan_kernel, dim3(1), dim3(1024), 0, st, p, int(chunks), bits);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(plan_place_kernel, grid, dim3(256), 0, st, p, chunk, chunks, bits);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.T == 0 || p.D == 0) return e;
+  const int64_t tile_units = (p.M_total / 128) * ((p.D / 128 + 15) / 16);
+  const int64_t blocks = tile_units + (p.T * ((p.D + 1023) / 1024) + 3) / 4;
+  hipLaunchKernelGGL(move_kernel, dim3(grid_of(blocks, 256)), dim3(256), 0, st, p, tile_units, blocks);
+  return hipGetLastError();
+}
+
+}  // namespace fp8q

@@ -1,0 +1,127 @@
+// Internal launchers behind include/fp8q_front.h, and the sizes of their
+// workspaces.  Arguments are validated by abi_front.cpp before any of these is
+// called; each enqueues on `st` and returns the launch status without
+// synchronising.
+#pragma once
+
+#include "../ffn/launch_plan.h"
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+namespace fp8q {
+
+struct NormArgs {
+  const void* x; int64_t ld_x;
+  const void* r; int64_t ld_r;    // or nullptr
+  int64_t M, D;
+  const void* weight;
+  float eps;
+  void* h; int64_t ld_h;          // or nullptr
+  float* rstd;                    // or nullptr
+  void* y; int64_t ld_y;          // or nullptr
+  uint8_t* q; int64_t ld_q; float* scales;
+  uint8_t* q_t; int64_t ld_qt; float* scales_t;   // or nullptr
+};
+hipError_t launch_fp8_rmsnorm(const NormArgs& p, bool x_bf16, bool w_bf16, int mode, hipStream_t st);
+hipError_t launch_int8_rmsnorm(const NormArgs& p, bool x_bf16, bool w_bf16, hipStream_t st);
+
+struct NormBwdArgs {
+  const void* dy; int64_t ld_dy;
+  const void* h; int64_t ld_h;
+  int64_t M, D;
+  const void* weight;
+  const float* rstd;
+  const void* dh; int64_t ld_dh;  // or nullptr
+  void* dx; int64_t ld_dx;
+  float* dw; bool accumulate;
+  float* part;                    // [norm_bwd_parts(M, D)][D rounded up to 8]
+};
+hipError_t launch_rmsnorm_backward(const NormBwdArgs& p, bool x_bf16, bool w_bf16, hipStream_t st);
+
+// The widest row that a workgroup keeps in registers.
+constexpr int64_t kMaxNormD = 32768;
+
+// Threads that share a row, and rows that a workgroup of them has in hand.
+inline int norm_bwd_threads(int64_t D) { return D <= 1024 ? 64 : D <= 8192 ? 256 : 1024; }
+
+// Workgroups of the gradient kernel, each of which leaves one partial sum of
+// dw per column.
+inline int64_t norm_bwd_parts(int64_t M, int64_t D) {
+  const int64_t rows = norm_bwd_threads(D) == 64 ? 4 : 1, want = (M + rows - 1) / rows;
+  const int64_t most = norm_bwd_threads(D) == 1024 ? 256 : 512;
+  return want < most ? want : most;
+}
+inline int64_t norm_bwd_workspace(int64_t M, int64_t D) { return norm_bwd_parts(M, D) * ((D + 7) / 8 * 8) * 4; }
+
+// ---- routing ---------------------------------------------------------------------
+
+constexpr int64_t kMaxExperts = 1024;
+constexpr int kMaxChosen = 32;    // experts of a token
+
+struct RouteArgs {
+  const void* logits; int64_t ld_z;
+  int64_t T, E, k;
+  const uint8_t* valid;           // or nullptr
+  bool renormalize;
+  float* weights; int32_t* experts; int32_t* counts; float* loss; float* slope;
+  float* part_p; int32_t* part_c; int32_t* part_n; float* part_l;   // sums of each workgroup
+};
+hipError_t launch_moe_route(const RouteArgs& p, bool bf16, hipStream_t st);
+
+struct RouteBwdArgs {
+  const void* logits; int64_t ld_z;
+  int64_t T, E, k;
+  const int32_t* experts; const float* slope;
+  const float* dweights; const float* dloss;      // or nullptr
+  bool renormalize;
+  void* dlogits; int64_t ld_dz;
+};
+hipError_t launch_moe_route_backward(const RouteBwdArgs& p, bool bf16, hipStream_t st);
+
+// Tokens that a workgroup has in hand.
+inline int64_t route_tokens(int64_t E) { return E <= 64 ? 32 : E <= 128 ? 16 : E <= 256 ? 8 : 4; }
+
+// Workgroups of the forward kernel.  One alone finishes the sums itself.
+inline int64_t route_parts(int64_t T, int64_t E) {
+  const int64_t turns = (T + route_tokens(E) - 1) / route_tokens(E);
+  return turns <= 2 ? 1 : turns < 512 ? turns : 512;
+}
+// Sums of p, counts, tokens, and the loss's shares of up to 16 workgroups.
+inline int64_t route_workspace(int64_t T, int64_t E) {
+  const int64_t parts = route_parts(T, E);
+  return parts == 1 ? 0 : parts * E * 8 + (parts + 3) / 4 * 16 + 64;
+}
+
+// ---- dispatch --------------------------------------------------------------------
+
+struct DispatchArgs {
+  const int32_t* experts;
+  int64_t T, k, E;
+  const uint8_t* q; int64_t ld_q; const float* scales;
+  int64_t D, M_total;
+  uint8_t* a; int64_t ld_a; float* a_scales;
+  int32_t* group_of_mtile; int32_t* row_of_slot; int32_t* token_of_row;
+  int32_t* hist;                  // [dispatch_chunks(T k)][E], or nullptr with one chunk
+};
+hipError_t launch_moe_dispatch(const DispatchArgs& p, hipStream_t st);
+
+// Slots whose ranks one workgroup alone finds.
+constexpr int64_t kDispatchAlone = 8192;
+
+// Slots of one wave, whole steps of 64, of which up to 128 waves share the rest.
+inline int64_t dispatch_chunk(int64_t slots) {
+  const int64_t steps = (slots + 64 * 128 - 1) / (64 * 128);
+  return 64 * (steps > 4 ? steps : 4);
+}
+inline int64_t dispatch_chunks(int64_t slots) {
+  return slots <= kDispatchAlone ? 0 : (slots - 1) / dispatch_chunk(slots) + 1;
+}
+inline int64_t dispatch_workspace(int64_t slots, int64_t E) { return dispatch_chunks(slots) * E * 4; }
+
+// Whole 128-row tiles that the slots take at most: each of n experts wastes up to 127 rows.
+inline int64_t dispatch_max_rows(int64_t slots, int64_t E) {
+  return (slots + 127 * (slots < E ? slots : E)) / 128 * 128;
+}
+
+}  // namespace fp8q

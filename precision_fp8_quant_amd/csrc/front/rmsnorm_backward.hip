@@ -1,0 +1,151 @@
+// Gradient of the root-mean-square norm.
+//
+//   xhat = h rstd,  g = dy w,  dx = rstd (g - xhat sum(g xhat) / D) + dh
+//   dw[d] = sum_m dy[m][d] xhat[m][d]
+// One pass over dy, h and dh: a row is held in registers between its sum and
+// dx, by TPR threads of R runs of 8 elements (run i of thread t: columns
+// 8 (i TPR + t)), and each thread keeps the sums of dw of its own columns over
+// all rows of its workgroup.  The workgroups' sums (in the workspace, one row
+// each) are added by a second kernel, in a fixed order: no atomics.
+#include "front_launch.h"
+#include "lanes.h"
+#include "row_io.h"
+
+namespace fp8q {
+namespace {
+
+template <typename T, typename W, int TPR, int R>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel(NormBwdArgs p) {
+  constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
+  __shared__ float part[NT / 64];
+  const int t = threadIdx.x & (TPR - 1);
+  const T* __restrict__ dy = static_cast<const T*>(p.dy);
+  const T* __restrict__ h = static_cast<const T*>(p.h);
+  const T* __restrict__ dh = static_cast<const T*>(p.dh);
+  T* __restrict__ dx = static_cast<T*>(p.dx);
+  const W* __restrict__ weight = static_cast<const W*>(p.weight);
+  const float inv_d = 1.0f / float(p.D);
+  Row8<W> wr[R];
+  float acc[R][8];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    load_raw(wr[i], weight, int64_t(i * TPR + t) * 8, p.D);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+  }
+  // the last rows' threads stay for the barriers (TPR > 64) and lane exchanges of the others
+  for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < p.M; row0 += int64_t(gridDim.x) * RPB) {
+    const int64_t row = row0 + threadIdx.x / TPR;
+    const int64_t D = row < p.M ? p.D : 0;
+    Row8<T> yr[R], hr[R], er[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) load_raw(yr[i], dy + row * p.ld_dy, int64_t(i * TPR + t) * 8, D);
+#pragma unroll
+    for (int i = 0; i < R; ++i) load_raw(hr[i], h + row * p.ld_h, int64_t(i * TPR + t) * 8, D);
+    if (dh) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) load_raw(er[i], dh + row * p.ld_dh, int64_t(i * TPR + t) * 8, D);
+    }
+    const float rs = row < p.M ? p.rstd[row] : 0.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float z = yr[i].get(j) * (hr[i].get(j) * rs);
+        acc[i][j] += z;
+        sum = __builtin_fmaf(z, wr[i].get(j), sum);
+      }
+    const float c = row_sum<TPR>(sum, part) * inv_d;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = rs * __builtin_fmaf(-(hr[i].get(j) * rs), c, yr[i].get(j) * wr[i].get(j));
+        if (dh) v[j] += er[i].get(j);
+      }
+      store_raw(dx + row * p.ld_dx, int64_t(i * TPR + t) * 8, D, v);
+    }
+    if constexpr (TPR > 64) __syncthreads();       // `part` is reused by the next row
+  }
+  const int64_t dp = (p.D + 7) / 8 * 8;
+  float* out = p.part + int64_t(blockIdx.x) * dp;
+  if constexpr (RPB > 1) {                         // the rows of the workgroup meet in LDS
+    __shared__ float sums[RPB][R * TPR * 8];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sums[threadIdx.x / TPR][(i * TPR + t) * 8 + j] = acc[i][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < dp; c += NT) {
+      float s = sums[0][c];
+#pragma unroll
+      for (int k = 1; k < RPB; ++k) s += sums[k][c];
+      out[c] = s;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if ((i * TPR + t) * 8 < dp) store8(out + (i * TPR + t) * 8, acc[i]);
+  }
+}
+
+// dw[c] (+)= sum over the parts, 64 columns a workgroup, 16 waves that take the
+// parts in turn.
+__global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restrict__ part, int64_t parts, int64_t ld,
+                                                           int64_t cols, float* __restrict__ dw, bool accumulate) {
+  __shared__ float sums[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int64_t c0 = int64_t(blockIdx.x) * 64; c0 < cols; c0 += int64_t(gridDim.x) * 64) {
+    const int64_t c = c0 + lane;
+    float s = 0.0f;
+    if (c < cols) {
+#pragma unroll 8
+      for (int64_t k = wave; k < parts; k += 16) s += part[k * ld + c];
+    }
+    sums[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < cols) {
+#pragma unroll
+      for (int w = 1; w < 16; ++w) s += sums[w][lane];
+      dw[c] = accumulate ? dw[c] + s : s;
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, typename W, int TPR, int R>
+void launch_rows(const NormBwdArgs& p, int64_t parts, hipStream_t st) {
+  constexpr int NT = TPR < 256 ? 256 : TPR;
+  hipLaunchKernelGGL((rmsnorm_backward_kernel<T, W, TPR, R>), dim3(unsigned(parts)), dim3(NT), 0, st, p);
+}
+
+template <typename T, typename W>
+hipError_t launch(const NormBwdArgs& p, hipStream_t st) {
+  const int64_t parts = norm_bwd_parts(p.M, p.D);  // norm_bwd_threads() says TPR
+  if (parts > 0) {
+    if (p.D <= 512) launch_rows<T, W, 64, 1>(p, parts, st);
+    else if (p.D <= 1024) launch_rows<T, W, 64, 2>(p, parts, st);
+    else if (p.D <= 2048) launch_rows<T, W, 256, 1>(p, parts, st);
+    else if (p.D <= 4096) launch_rows<T, W, 256, 2>(p, parts, st);
+    else if (p.D <= 8192) launch_rows<T, W, 256, 4>(p, parts, st);
+    else if (p.D <= 16384) launch_rows<T, W, 1024, 2>(p, parts, st);
+    else launch_rows<T, W, 1024, 4>(p, parts, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (parts == 0 && p.accumulate) return hipSuccess;
+  hipLaunchKernelGGL(column_sums_kernel, dim3(unsigned((p.D + 63) / 64)), dim3(1024), 0, st, p.part, parts, (p.D + 7) / 8 * 8,
+                     p.D, p.dw, p.accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm_backward(const NormBwdArgs& p, bool x_bf16, bool w_bf16, hipStream_t st) {
+  if (x_bf16) return w_bf16 ? launch<uint16_t, uint16_t>(p, st) : launch<uint16_t, float>(p, st);
+  return w_bf16 ? launch<float, uint16_t>(p, st) : launch<float, float>(p, st);
+}
+
+}  // namespace fp8q

@@ -1,0 +1,267 @@
+"""include/fp8q_front.h: every entry point is exported and bound, arguments are rejected before anything is launched, and
+the 64-bit definitions of oracle/front.py hold against differences (CPU only: no call here reaches a kernel launch)."""
+
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import front as orf
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "fp8q_front.h")
+
+fp8q = pytest.importorskip("precision_fp8_quant_amd", reason="libfp8q.so not built")
+from precision_fp8_quant_amd import front  # noqa: E402
+
+# fake 16-byte aligned device addresses, 256 MiB apart
+X, R, W, H, S, Y, Q, SQ, QT, ST, WS = (0x10000000 * i for i in range(1, 12))
+HUGE = 1 << 62
+MAX = (1 << 63) - 1
+
+
+def test_every_declared_symbol_is_exported_and_bound():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = set(re.findall(r"^\s*int\s+(\w+)\s*\(", text, flags=re.M))
+    sizes = set(re.findall(r"^\s*int64_t\s+(\w+)\s*\(", text, flags=re.M))
+    assert names == set(front.SIGNATURES) == {"fp8_rmsnorm", "int8_rmsnorm", "rmsnorm_backward", "moe_route",
+                                              "moe_route_backward", "fp8_moe_dispatch"}
+    assert sizes == set(front.SIZES)
+    raw = ctypes.CDLL(fp8q.LIB_PATH)
+    assert all(hasattr(raw, n) for n in names | sizes)
+    assert all(callable(getattr(fp8q, n)) for n in names)
+
+
+def _fp8(**kw):
+    v = dict(x=X, ldx=256, r=R, ldr=256, xdt=fp8q.BF16, m=200, d=256, w=W, wdt=fp8q.F32, eps=1e-6, mode=0, h=H, ldh=256,
+             rstd=S, y=Y, ldy=256, q=Q, ldq=256, s=SQ, qt=QT, ldqt=256, st=ST)
+    v.update(kw)
+    return fp8q.lib.fp8_rmsnorm(v["x"], v["ldx"], v["r"], v["ldr"], v["xdt"], v["m"], v["d"], v["w"], v["wdt"], v["eps"],
+                                v["mode"], v["h"], v["ldh"], v["rstd"], v["y"], v["ldy"], v["q"], v["ldq"], v["s"],
+                                v["qt"], v["ldqt"], v["st"], None)
+
+
+BOTH = [
+    ("OK", dict(m=0, x=None)),
+    ("ERR_ARG", dict(xdt=2)), ("ERR_ARG", dict(wdt=-1)), ("ERR_ARG", dict(eps=0.0)), ("ERR_ARG", dict(eps=-1e-6)),
+    ("ERR_ARG", dict(eps=float("nan"))), ("ERR_ARG", dict(eps=float("inf"))), ("ERR_ARG", dict(r=None)),   # h without a sum
+    ("ERR_SHAPE", dict(m=-1)), ("ERR_SHAPE", dict(d=-128)),
+    *[("ERR_NULL", {n: None}) for n in ("x", "w", "h", "q", "s")],
+    *[("ERR_SHAPE", {n: 248}) for n in ("ldx", "ldr", "ldh", "ldy")], ("ERR_SHAPE", dict(ldq=240)),
+    ("ERR_ALIGN", dict(x=X + 8)), ("ERR_ALIGN", dict(w=W + 4)), ("ERR_ALIGN", dict(ldr=260)), ("ERR_ALIGN", dict(ldq=264)),
+    ("ERR_ALIGN", dict(rstd=S + 4)), ("ERR_ALIGN", dict(y=Y + 2)), ("ERR_ALIGN", dict(ldh=257)), ("ERR_ALIGN", dict(s=SQ + 8)),
+    ("ERR_ALIAS", dict(h=X)), ("ERR_ALIAS", dict(h=R + 256)), ("ERR_ALIAS", dict(y=H + 512 * 199)), ("ERR_ALIAS", dict(q=W)),
+    ("ERR_ALIAS", dict(s=Q + 256)), ("ERR_ALIAS", dict(rstd=SQ)),
+]
+
+
+@pytest.mark.parametrize("want, kw", BOTH + [
+    ("OK", dict(d=0, q=None)), ("ERR_ARG", dict(mode=2)),
+    ("ERR_NULL", dict(qt=None)), ("ERR_NULL", dict(st=None)), ("ERR_NULL", dict(rstd=None)),   # both tilings need it
+    ("ERR_SHAPE", dict(ldqt=208)),                     # whole 128-row tiles: 256 columns for 200 rows
+    ("ERR_SHAPE", dict(m=MAX, ldx=256)), ("ERR_SHAPE", dict(m=HUGE)),
+    ("ERR_ALIGN", dict(ldqt=264)), ("ERR_ALIGN", dict(st=ST + 4)),
+    ("ERR_UNSUPPORTED", dict(d=192)),
+    ("ERR_UNSUPPORTED", dict(d=32896, **{n: 32896 for n in ("ldx", "ldr", "ldh", "ldy", "ldq")})),
+    ("ERR_ALIAS", dict(qt=Q + 255 * 256)),             # a padded row of q
+    ("ERR_ALIAS", dict(st=SQ + 2 * 254 * 4)),
+])
+def test_fp8_rmsnorm_validation(want, kw):
+    assert _fp8(**kw) == getattr(fp8q, want), kw
+
+
+def _int8(**kw):
+    v = dict(x=X, ldx=256, r=R, ldr=256, xdt=fp8q.BF16, m=200, d=250, w=W, wdt=fp8q.BF16, eps=1e-6, h=H, ldh=256, rstd=S, y=Y,
+             ldy=256, q=Q, ldq=256, s=SQ)
+    v.update(kw)
+    return fp8q.lib.int8_rmsnorm(v["x"], v["ldx"], v["r"], v["ldr"], v["xdt"], v["m"], v["d"], v["w"], v["wdt"], v["eps"],
+                                 v["h"], v["ldh"], v["rstd"], v["y"], v["ldy"], v["q"], v["ldq"], v["s"], None)
+
+
+@pytest.mark.parametrize("want, kw", BOTH + [
+    ("ERR_NULL", dict(d=0, s=None)),
+    ("ERR_UNSUPPORTED", dict(d=32769, **{n: 32784 for n in ("ldx", "ldr", "ldh", "ldy", "ldq")})),
+    ("ERR_SHAPE", dict(m=HUGE)),
+])
+def test_int8_rmsnorm_validation(want, kw):
+    assert _int8(**kw) == getattr(fp8q, want), kw
+
+
+def _bwd(**kw):
+    v = dict(dy=X, lddy=256, h=H, ldh=256, dt=fp8q.F32, m=200, d=250, w=W, wdt=fp8q.BF16, rstd=S, dh=R, lddh=256, dx=Y,
+             lddx=256, dw=Q, acc=0, ws=WS)
+    v.update(kw)
+    return fp8q.lib.rmsnorm_backward(v["dy"], v["lddy"], v["h"], v["ldh"], v["dt"], v["m"], v["d"], v["w"], v["wdt"],
+                                     v["rstd"], v["dh"], v["lddh"], v["dx"], v["lddx"], v["dw"], v["acc"], v["ws"], None)
+
+
+@pytest.mark.parametrize("want, kw", [
+    ("OK", dict(d=0, dw=None)), ("OK", dict(m=0, acc=1, dy=None, ws=None)),
+    ("ERR_ARG", dict(dt=2)), ("ERR_ARG", dict(wdt=2)), ("ERR_ARG", dict(acc=2)), ("ERR_ARG", dict(acc=-1)),
+    ("ERR_SHAPE", dict(m=-1)), ("ERR_SHAPE", dict(d=-1)), ("ERR_SHAPE", dict(m=HUGE)),
+    *[("ERR_NULL", {n: None}) for n in ("dy", "h", "w", "rstd", "dx", "dw", "ws")], ("ERR_NULL", dict(m=0, dw=None)),
+    *[("ERR_SHAPE", {n: 248}) for n in ("lddy", "ldh", "lddh", "lddx")],
+    *[("ERR_ALIGN", {n: v + 8}) for n, v in dict(dy=X, h=H, w=W, rstd=S, dh=R, dx=Y, dw=Q, ws=WS).items()],
+    ("ERR_ALIGN", dict(lddy=250)), ("ERR_ALIGN", dict(lddx=257)), ("ERR_ALIGN", dict(lddh=258)),
+    ("ERR_UNSUPPORTED", dict(d=32769, **{n: 32772 for n in ("lddy", "ldh", "lddh", "lddx")})),
+    ("ERR_ALIAS", dict(dx=X)), ("ERR_ALIAS", dict(dx=R)), ("ERR_ALIAS", dict(dw=W)), ("ERR_ALIAS", dict(ws=Q + 992)),
+    ("ERR_ALIAS", dict(ws=S + 784)),
+])
+def test_rmsnorm_backward_validation(want, kw):
+    assert _bwd(**kw) == getattr(fp8q, want), kw
+
+
+def _route(**kw):
+    v = dict(z=X, ldz=64, dt=fp8q.F32, t=300, e=60, k=8, valid=R, renorm=0, w=W, ex=H, c=S, loss=Y, slope=Q, ws=WS)
+    v.update(kw)
+    return fp8q.lib.moe_route(v["z"], v["ldz"], v["dt"], v["t"], v["e"], v["k"], v["valid"], v["renorm"], v["w"], v["ex"],
+                              v["c"], v["loss"], v["slope"], v["ws"], None)
+
+
+@pytest.mark.parametrize("want, kw", [
+    ("ERR_ARG", dict(dt=2)), ("ERR_ARG", dict(renorm=2)),
+    ("ERR_SHAPE", dict(t=-1)), ("ERR_SHAPE", dict(k=61)), ("ERR_SHAPE", dict(e=-1)), ("ERR_SHAPE", dict(ldz=56)),
+    ("ERR_UNSUPPORTED", dict(e=0, k=0)), ("ERR_UNSUPPORTED", dict(k=0)), ("ERR_UNSUPPORTED", dict(e=1025, ldz=1028)),
+    ("ERR_UNSUPPORTED", dict(k=33)), ("ERR_UNSUPPORTED", dict(t=1 << 28)), ("ERR_UNSUPPORTED", dict(t=MAX)),
+    *[("ERR_NULL", {n: None}) for n in ("z", "w", "ex", "c", "loss", "slope", "ws")], ("ERR_NULL", dict(t=0, loss=None)),
+    *[("ERR_ALIGN", {n: v + 4}) for n, v in dict(z=X, valid=R, w=W, ex=H, c=S, loss=Y, slope=Q, ws=WS).items()],
+    ("ERR_ALIGN", dict(ldz=62)),
+    ("ERR_ALIAS", dict(w=X + 256 * 299)), ("ERR_ALIAS", dict(ex=R)), ("ERR_ALIAS", dict(c=H + 300 * 32 - 16)),
+    ("ERR_ALIAS", dict(loss=Q)), ("ERR_ALIAS", dict(ws=S + 224)),
+])
+def test_moe_route_validation(want, kw):
+    assert _route(**kw) == getattr(fp8q, want), kw
+
+
+def _route_bwd(**kw):
+    v = dict(z=X, ldz=64, dt=fp8q.BF16, t=300, e=60, k=8, ex=H, slope=S, dw=W, dl=Y, renorm=1, dz=Q, lddz=64)
+    v.update(kw)
+    return fp8q.lib.moe_route_backward(v["z"], v["ldz"], v["dt"], v["t"], v["e"], v["k"], v["ex"], v["slope"], v["dw"],
+                                       v["dl"], v["renorm"], v["dz"], v["lddz"], None)
+
+
+@pytest.mark.parametrize("want, kw", [
+    ("OK", dict(t=0, z=None, dz=None)),
+    ("ERR_ARG", dict(dt=7)), ("ERR_ARG", dict(renorm=-1)),
+    ("ERR_SHAPE", dict(t=-1)), ("ERR_SHAPE", dict(e=7, k=8)), ("ERR_SHAPE", dict(ldz=56)), ("ERR_SHAPE", dict(lddz=56)),
+    ("ERR_UNSUPPORTED", dict(k=0)), ("ERR_UNSUPPORTED", dict(e=1032, ldz=1032, lddz=1032)), ("ERR_UNSUPPORTED", dict(t=HUGE)),
+    ("ERR_NULL", dict(z=None)), ("ERR_NULL", dict(ex=None)), ("ERR_NULL", dict(dz=None)), ("ERR_NULL", dict(slope=None)),
+    *[("ERR_ALIGN", {n: v + 8}) for n, v in dict(z=X, ex=H, slope=S, dw=W, dl=Y, dz=Q).items()],
+    ("ERR_ALIGN", dict(ldz=60)), ("ERR_ALIGN", dict(lddz=62)),
+    ("ERR_ALIAS", dict(dz=X)), ("ERR_ALIAS", dict(dz=W)), ("ERR_ALIAS", dict(dz=Y - 128 * 299)),
+])
+def test_moe_route_backward_validation(want, kw):
+    assert _route_bwd(**kw) == getattr(fp8q, want), kw
+
+
+def _dispatch(**kw):
+    v = dict(ex=X, t=2000, k=8, e=64, q=Q, ldq=256, s=S, d=256, m=24064, a=QT, lda=256, sa=ST, g=H, rs=Y, tr=R, ws=WS)
+    v.update(kw)
+    return fp8q.lib.fp8_moe_dispatch(v["ex"], v["t"], v["k"], v["e"], v["q"], v["ldq"], v["s"], v["d"], v["m"], v["a"],
+                                     v["lda"], v["sa"], v["g"], v["rs"], v["tr"], v["ws"], None)
+
+
+@pytest.mark.parametrize("want, kw", [
+    ("OK", dict(t=0, m=0, ex=None, q=None, a=None, g=None, tr=None)),
+    ("ERR_SHAPE", dict(t=-1)), ("ERR_SHAPE", dict(d=-128)), ("ERR_SHAPE", dict(m=24000)), ("ERR_SHAPE", dict(m=23936)),
+    ("ERR_SHAPE", dict(ldq=240)), ("ERR_SHAPE", dict(lda=128)),
+    ("ERR_UNSUPPORTED", dict(e=0)), ("ERR_UNSUPPORTED", dict(e=1025)), ("ERR_UNSUPPORTED", dict(k=33)),
+    ("ERR_UNSUPPORTED", dict(k=0)), ("ERR_UNSUPPORTED", dict(t=1 << 27)), ("ERR_UNSUPPORTED", dict(d=160)),
+    ("ERR_UNSUPPORTED", dict(m=1 << 31)),
+    *[("ERR_NULL", {n: None}) for n in ("ex", "q", "s", "a", "sa", "g", "rs", "tr", "ws")],
+    *[("ERR_ALIGN", {n: v + 4}) for n, v in dict(ex=X, q=Q, s=S, a=QT, sa=ST, g=H, rs=Y, tr=R, ws=WS).items()],
+    ("ERR_ALIGN", dict(ldq=264)), ("ERR_ALIGN", dict(lda=264)),
+    ("ERR_ALIAS", dict(a=Q + 256 * 1999)), ("ERR_ALIAS", dict(sa=S)), ("ERR_ALIAS", dict(rs=X + 63984)),
+    ("ERR_ALIAS", dict(tr=H)), ("ERR_ALIAS", dict(ws=Y)),
+])
+def test_dispatch_validation(want, kw):
+    assert _dispatch(**kw) == getattr(fp8q, want), kw
+
+
+def test_sizes():
+    lib = fp8q.lib
+    assert fp8q.moe_max_rows(2000, 8, 64) == 24064 and fp8q.moe_max_rows(0, 8, 64) == 0 and fp8q.moe_max_rows(1, 1, 64) == 128
+    assert lib.fp8q_moe_max_rows(1, 1, 1025) == lib.fp8q_moe_max_rows(-1, 1, 4) == lib.fp8q_moe_max_rows(1 << 30, 1, 4) == -1
+    assert lib.fp8q_rmsnorm_backward_workspace(1, 32769) == lib.fp8q_rmsnorm_backward_workspace(-1, 8) == -1
+    assert lib.fp8q_rmsnorm_backward_workspace(0, 8) == 0 and lib.fp8q_rmsnorm_backward_workspace(MAX, 32768) > 0
+    assert lib.fp8q_moe_route_workspace(1 << 31, 8) == -1 and lib.fp8q_moe_route_workspace(0, 8) == 0
+    assert lib.fp8q_moe_dispatch_workspace(1 << 30, 1, 8) == -1
+    with pytest.raises(ValueError, match="no such sizes"):
+        fp8q.moe_max_rows(5, 0, 8)
+    # every row that any choice of experts fills fits: all slots in as many experts as there are, one row over each tile
+    for slots, e in [(1, 1), (5, 64), (64, 64), (200, 64), (8192, 64), (129 * 3, 3)]:
+        used, counts = min(slots, e), [1] * min(slots, e)
+        for i in range(slots - used):
+            counts[(i // 128) % used] += 1
+        assert sum(-(-c // 128) * 128 for c in counts) <= lib.fp8q_moe_max_rows(slots, 1, e)
+
+
+def test_binding_names_what_is_wrong():
+    x, w = torch.zeros((4, 128)), torch.zeros(128)
+    idx = torch.zeros((4, 2), dtype=torch.int32)
+    for call in (lambda: fp8q.fp8_rmsnorm(x, w), lambda: fp8q.int8_rmsnorm(x, w), lambda: fp8q.moe_route(x, 2),
+                 lambda: fp8q.rmsnorm_backward(x, x, w, torch.zeros(4)), lambda: fp8q.moe_route_backward(x, idx),
+                 lambda: fp8q.fp8_moe_dispatch(idx, x.to(torch.uint8), torch.zeros(1, 4), 8)):
+        with pytest.raises(ValueError, match="must be a device tensor"):
+            call()
+
+
+# --- the definitions themselves -------------------------------------------
+
+def test_norm_gradient_against_differences():
+    """Central differences of sum(y dy + h dh) with step 1e-6: truncation and rounding under 1e-8 for values of order 1."""
+    rng = np.random.default_rng(3)
+    h, w, dy, dh = rng.standard_normal((3, 7)), rng.standard_normal(7), rng.standard_normal((3, 7)), rng.standard_normal((3, 7))
+    eps, step = 0.1, 1e-6
+    f = lambda h_, w_: float((orf.norm(h_, w_, eps) * dy).sum() + (h_ * dh).sum())      # noqa: E731
+    dx, dw = orf.norm_backward(dy, h, w, orf.rstd(h, eps), dh)
+    for i in np.ndindex(h.shape):
+        d = np.zeros_like(h)
+        d[i] = step
+        assert abs((f(h + d, w) - f(h - d, w)) / (2 * step) - dx[i]) < 1e-8
+    for i in range(7):
+        d = np.zeros_like(w)
+        d[i] = step
+        assert abs((f(h, w + d) - f(h, w - d)) / (2 * step) - dw[i]) < 1e-8
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_route_gradient_against_differences(renormalize):
+    rng = np.random.default_rng(4)
+    z = rng.standard_normal((5, 6))
+    z[1, 2] = z[3, :4] = -np.inf                          # one expert out, and fewer than k left
+    valid = np.array([1, 1, 0, 1, 1])
+    w, ex, counts, loss, slope = orf.route(z, 3, valid, renormalize)
+    assert ex[2].tolist() == [-1, -1, -1] and ex[3, 2] == -1 and counts.sum() == 11
+    dw, dloss, step = rng.standard_normal((5, 3)), 0.7, 1e-6
+    assert abs(orf.route_value(z, ex, slope, dw, dloss, renormalize) - (dw * w).sum() - dloss * loss) < 1e-12
+    dz = orf.route_backward(z, ex, slope, dw, dloss, renormalize)
+    for i in np.ndindex(z.shape):
+        if not np.isfinite(z[i]):
+            assert dz[i] == 0
+            continue
+        d = np.zeros_like(z)
+        d[i] = step
+        num = (orf.route_value(z + d, ex, slope, dw, dloss, renormalize)
+               - orf.route_value(z - d, ex, slope, dw, dloss, renormalize)) / (2 * step)
+        assert abs(num - dz[i]) < 1e-8
+
+
+def test_balance_loss_of_even_and_of_lopsided_choices():
+    """1 where all experts share evenly, E where one has everything."""
+    even = np.full((6, 3), 0.0)
+    even[np.arange(6), np.arange(6) % 3] = 1e-9
+    assert abs(orf.route(even, 1)[3] - 1.0) < 1e-6
+    one = np.zeros((4, 5))
+    one[:, 2] = 50.0
+    assert abs(orf.route(one, 1)[3] - 5.0) < 1e-12
+
+
+def test_dispatch_of_a_worked_example():
+    """Experts 1, 0 and 1 of two tokens: expert 0 has one row in tile 0, expert 1 two in tile 1."""
+    group, rows, tokens = orf.dispatch(np.array([[1, 0], [1, -1]]), 3, 384)
+    assert group.tolist() == [0, 1, -1] and rows.tolist() == [[128, 0], [129, -1]]
+    assert tokens[0] == 0 and tokens[128] == 0 and tokens[129] == 1 and (tokens >= 0).sum() == 3
