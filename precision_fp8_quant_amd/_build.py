@@ -36,13 +36,13 @@ PER_SOURCE_FLAGS = {"gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
                     "ffn/fp8_gated.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
-# The native call path of ffn.py: a CPython extension against torch's headers,
-# linked to libfp8q.so beside it.  The package works without it.
-BINDING_SRC = os.path.join(CSRC, "ffn", "binding.cpp")
+# The native call path of ffn.py and front.py: a CPython extension against torch's
+# headers, linked to libfp8q.so beside it.  The package works without it.
+BINDING_SOURCES = ["ffn/binding.cpp", "front/binding.cpp"]
 BINDING_PATH = os.path.join(PKG_DIR, "_ffn_call.so")
 
 
-def _binding_command(out):
+def _binding_command(src, out):
     import sysconfig
 
     import torch
@@ -52,14 +52,14 @@ def _binding_command(out):
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
             "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
-            "-isystem", os.path.join(rocm, "include"), BINDING_SRC, "-o", out]
+            "-isystem", os.path.join(rocm, "include"), os.path.join(CSRC, src), "-o", out]
 
 
-def _link_binding(obj, verbose):
+def _link_binding(objs, verbose):
     import torch
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING_PATH + ".tmp"
-    _run([os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, "-L", libs, "-ltorch", "-ltorch_cpu", "-ltorch_python",
+    _run([os.environ.get("CXX", "g++"), "-shared", *objs, "-o", tmp, "-L", libs, "-ltorch", "-ltorch_cpu", "-ltorch_python",
           "-lc10", "-lc10_hip", "-L", PKG_DIR, "-lfp8q", "-Wl,-rpath,$ORIGIN"], verbose)
     os.replace(tmp, BINDING_PATH)
 
@@ -97,17 +97,18 @@ def build(verbose=False, extra_flags=()):
     """libfp8q.so and, where torch is installed, the native call path (always recompiles).  The library is complete
     when the call path fails to build, which is still an error."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    binding = os.path.join(BUILD_DIR, "ffn_binding.cpp.o")
-    with ThreadPoolExecutor(max_workers=1) as ex:  # beside the library's sources
+    objs = [os.path.join(BUILD_DIR, src.replace("/", "_") + ".o") for src in BINDING_SOURCES]
+    with ThreadPoolExecutor(max_workers=len(objs)) as ex:  # beside the library's sources
         try:
-            compiled = ex.submit(_run, _binding_command(binding), verbose)
+            compiled = [ex.submit(_run, _binding_command(src, obj), verbose) for src, obj in zip(BINDING_SOURCES, objs)]
         except ImportError as e:
-            compiled = None
+            compiled = []
             print(f"{os.path.basename(BINDING_PATH)} is not built: {e}", flush=True)
         build_library(verbose, extra_flags)
     if compiled:
-        compiled.result()
-        _link_binding(binding, verbose)
+        for c in compiled:
+            c.result()
+        _link_binding(objs, verbose)
     return LIB_PATH
 
 

@@ -23,6 +23,7 @@ template <> struct Row8<uint16_t> {
   u32x4 w;
   __device__ __forceinline__ void load(const uint16_t* p) { w = *reinterpret_cast<const u32x4*>(p); }
   __device__ __forceinline__ void zero() { w = u32x4{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(w)); }
   __device__ __forceinline__ float get(int i) const {
     return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
   }
@@ -34,6 +35,7 @@ template <> struct Row8<float> {
     b = reinterpret_cast<const v4f*>(p)[1];
   }
   __device__ __forceinline__ void zero() { a = b = v4f{0.0f, 0.0f, 0.0f, 0.0f}; }
+  __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(a), "+v"(b)); }
   __device__ __forceinline__ float get(int i) const { return i < 4 ? a[i] : b[i - 4]; }
 };
 

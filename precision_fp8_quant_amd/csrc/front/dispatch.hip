@@ -8,8 +8,8 @@
 // lane's place is the expert's running count plus its equals in lower lanes.
 //   up to 8192 slots   one workgroup: counts of its 16 waves' chunks, their
 //                      prefix sums and the tile map, the rows
-//   beyond             the three steps as kernels of their own, over up to 128
-//                      chunks
+//   beyond             two kernels over up to 128 chunks: their counts; then the
+//                      rows, every workgroup summing all counts for itself
 // Then one kernel moves codes and scales: a token's row is read once and
 // written to its k places; scales, which lie transposed, are written in runs of
 // a tile's 128 rows, with the padding rows of the tile.
@@ -22,40 +22,57 @@ namespace {
 
 constexpr uint32_t kZeroScaleBits = 0x00800000u;   // 2^-126: the scale of a row of zeros
 
-__device__ __forceinline__ int expert_at(const DispatchArgs& p, int64_t slot, int64_t end) {
-  if (slot >= end) return -1;
-  const int e = p.experts[slot];
-  return e >= 0 && e < int(p.E) ? e : -1;
+constexpr int kSteps = 8;     // steps of 64 slots whose experts a wave loads together
+
+// The experts of slots [s, s + 64 kSteps) up to `end`, a lane's at s + 64 i + lane; -1 for no expert.
+__device__ __forceinline__ void load_experts(const DispatchArgs& p, int64_t s, int64_t end, int (&e)[kSteps]) {
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int64_t slot = s + 64 * i + (threadIdx.x & 63);
+    e[i] = slot < end ? p.experts[slot] : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) e[i] = uint32_t(e[i]) < uint32_t(p.E) ? e[i] : -1;
 }
 
 // Adds the experts of slots [begin, end) to count[], by one wave.
 __device__ __forceinline__ void count_chunk(const DispatchArgs& p, int64_t begin, int64_t end, int* count) {
-  for (int64_t s = begin; s < end; s += 64) {
-    const int e = expert_at(p, s + (threadIdx.x & 63), end);
-    if (e >= 0) atomicAdd(&count[e], 1);           // integers: the order does not matter
+  for (int64_t s = begin; s < end; s += 64 * kSteps) {
+    int e[kSteps];
+    load_experts(p, s, end, e);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+      if (e[i] >= 0) atomicAdd(&count[e[i]], 1);   // integers: the order does not matter
   }
 }
 
-// The rows of slots [begin, end), by one wave; next[e] is e's next row, in LDS
-// that no other wave writes.
-__device__ __forceinline__ void place_chunk(const DispatchArgs& p, int64_t begin, int64_t end, int bits, int* next) {
+// The rows of slots [begin, end), by one wave, whose first experts are in e;
+// next[x] is expert x's next row, in LDS that no other wave writes.
+__device__ __forceinline__ void place_chunk(const DispatchArgs& p, int64_t begin, int64_t end, int bits, int* next,
+                                            int (&e)[kSteps]) {
   const int lane = threadIdx.x & 63;
-  for (int64_t s = begin; s < end; s += 64) {      // uniform over the wave
-    const int64_t slot = s + lane;
-    const int e = expert_at(p, slot, end);
-    uint64_t same = __ballot(e >= 0);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t one = __ballot((e >> b) & 1);
-      same &= (e >> b) & 1 ? one : ~one;
+  const uint64_t below_mask = (uint64_t(1) << lane) - 1;
+  for (int64_t s = begin; s < end; s += 64 * kSteps) {     // uniform over the wave
+    if (s > begin) load_experts(p, s, end, e);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int64_t slot = s + 64 * i + lane;
+      if (s + 64 * i >= end) break;                // uniform over the wave
+      uint64_t same = __ballot(e[i] >= 0);
+      for (int b = 0; b < bits; ++b) {
+        const bool set = (e[i] >> b) & 1;
+        const uint64_t one = __ballot(set);
+        same &= set ? one : ~one;
+      }
+      const uint64_t below = same & below_mask;
+      int row = -1;
+      if (e[i] >= 0) row = next[e[i]] + __popcll(below);
+      asm volatile("" ::: "memory");               // the wave's reads come before its writes (LDS keeps their order)
+      if (e[i] >= 0 && below == 0) next[e[i]] = row + __popcll(same);
+      asm volatile("" ::: "memory");
+      if (slot < end) p.row_of_slot[slot] = row;
+      if (e[i] >= 0) p.token_of_row[row] = int32_t(slot / p.k);
     }
-    const uint64_t below = (uint64_t(1) << lane) - 1;
-    int row = -1;
-    if (e >= 0) row = next[e] + __popcll(same & below);
-    asm volatile("" ::: "memory");                 // the wave's reads come before its writes (LDS keeps their order)
-    if (e >= 0 && (same & below) == 0) next[e] = row + __popcll(same);
-    asm volatile("" ::: "memory");
-    if (slot < end) p.row_of_slot[slot] = row;
-    if (e >= 0) p.token_of_row[row] = int32_t(slot / p.k);
   }
 }
 
@@ -106,8 +123,10 @@ __global__ __launch_bounds__(1024) void plan_kernel(DispatchArgs p, int chunk, i
   const int t = threadIdx.x, wave = t >> 6, E = int(p.E);
   const int64_t slots = p.T * p.k, begin = int64_t(wave) * chunk;
   const int64_t end = begin + chunk < slots ? begin + chunk : slots;
-  for (int i = t; i < 16 * E; i += 1024) next[i / E][i % E] = 0;
+  for (int e = t & 63; e < E; e += 64) next[wave][e] = 0;
   __syncthreads();
+  int first_experts[kSteps];
+  load_experts(p, begin, end, first_experts);
   count_chunk(p, begin, end, next[wave]);
   __syncthreads();
   int count = 0;
@@ -127,7 +146,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(DispatchArgs p, int chunk, i
     }
   }
   write_maps(p, count, first, used, place);        // its barrier is also that of next[]
-  place_chunk(p, begin, end, bits, next[wave]);
+  place_chunk(p, begin, end, bits, next[wave], first_experts);
 }
 
 __global__ __launch_bounds__(256) void plan_count_kernel(DispatchArgs p, int64_t chunk, int64_t chunks) {
@@ -145,56 +164,53 @@ __global__ __launch_bounds__(256) void plan_count_kernel(DispatchArgs p, int64_t
     for (int e = lane; e < E; e += 64) p.hist[c * E + e] = count[wave][e];
 }
 
-// hist[c][e] becomes the first row of expert e's slots in chunk c.  Up to 16
-// threads (1024 over E rounded up to a power of two) take an expert's chunks in
-// consecutive pieces.
-__global__ __launch_bounds__(1024) void plan_scan_kernel(DispatchArgs p, int chunks, int log_e) {
-  __shared__ int sums[1024];
-  __shared__ int firsts[kMaxExperts];
+// 16 chunks a workgroup.  Up to 16 threads (1024 over E rounded up to a power
+// of two) sum an expert's counts over consecutive pieces of the chunks: all of
+// them for the first rows of the experts, those before the workgroup's for its
+// own.  The first workgroup also writes the maps.
+__global__ __launch_bounds__(1024) void plan_place_kernel(DispatchArgs p, int64_t chunk, int chunks, int bits) {
+  __shared__ int next[16][kMaxExperts];
   __shared__ int place[kMaxExperts][2];
   __shared__ int wave_sum[16];
-  const int t = threadIdx.x, E = int(p.E), ep = 1 << log_e, share = log_e < 6 ? 16 : 1024 >> log_e;
-  const int e = t & (ep - 1), piece = t >> log_e, len = (chunks + share - 1) / share;
+  int* sums = next[0];                             // [2][1024], before next[] is filled
+  const int t = threadIdx.x, wave = t >> 6, E = int(p.E), ep = 1 << bits, share = bits < 6 ? 16 : 1024 >> bits;
+  const int mine = blockIdx.x * 16, c = mine + wave;
+  const int64_t slots = p.T * p.k, begin = c * chunk, end = begin + chunk < slots ? begin + chunk : slots;
+  int experts[kSteps];
+  load_experts(p, begin, end, experts);
+  const int e = t & (ep - 1), piece = t >> bits, len = (chunks + share - 1) / share;
   const int c0 = piece * len, c1 = c0 + len < chunks ? c0 + len : chunks;
-  int sum = 0;
-  const bool busy = e < E && piece < share;
-  if (busy) {
+  int all = 0, before = 0;
+  if (e < E && piece < share) {
 #pragma unroll 8
-    for (int c = c0; c < c1; ++c) sum += p.hist[int64_t(c) * E + e];
-  }
-  sums[t] = sum;
-  __syncthreads();
-  int count = 0;
-  if (t < E)
-    for (int s = 0; s < share; ++s) count += sums[s * ep + t];
-  int used;
-  const int first = block_exclusive((count + 127) >> 7, wave_sum, &used);
-  if (t < E) firsts[t] = first;
-  __syncthreads();
-  if (busy) {
-    int row = firsts[e] * 128;
-    for (int s = 0; s < piece; ++s) row += sums[s * ep + e];
-#pragma unroll 8
-    for (int c = c0; c < c1; ++c) {
-      const int n = p.hist[int64_t(c) * E + e];
-      p.hist[int64_t(c) * E + e] = row;
-      row += n;
+    for (int i = c0; i < c1; ++i) {
+      const int n = p.hist[int64_t(i) * E + e];
+      all += n;
+      before += i < mine ? n : 0;
     }
   }
-  write_maps(p, count, first, used, place);
-}
-
-__global__ __launch_bounds__(256) void plan_place_kernel(DispatchArgs p, int64_t chunk, int64_t chunks, int bits) {
-  __shared__ int next[4][kMaxExperts];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, E = int(p.E);
-  const int64_t c = int64_t(blockIdx.x) * 4 + wave;
-  if (c < chunks)
-    for (int e = lane; e < E; e += 64) next[wave][e] = p.hist[c * E + e];
+  sums[t] = all;
+  sums[1024 + t] = before;
   __syncthreads();
-  if (c < chunks) {
-    const int64_t slots = p.T * p.k, end = (c + 1) * chunk < slots ? (c + 1) * chunk : slots;
-    place_chunk(p, c * chunk, end, bits, next[wave]);
+  all = before = 0;
+  if (t < E)
+    for (int s = 0; s < share; ++s) {
+      all += sums[s * ep + t];
+      before += sums[1024 + s * ep + t];
+    }
+  int used;
+  const int first = block_exclusive((all + 127) >> 7, wave_sum, &used);   // its barrier: sums[] has been read
+  if (t < E) {
+    int row = first * 128 + before;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      next[w][t] = row;
+      if (mine + w < chunks) row += p.hist[int64_t(mine + w) * E + t];
+    }
   }
+  if (blockIdx.x == 0) write_maps(p, all, first, used, place);
+  __syncthreads();
+  place_chunk(p, begin, end, bits, next[wave], experts);
 }
 
 // Work units: first every tile in pieces of 16 groups (2048 codes of a row),
@@ -223,7 +239,7 @@ __global__ __launch_bounds__(256) void move_kernel(DispatchArgs p, int64_t tile_
       const int64_t pieces = (p.D + 1023) >> 10, w = (u - tile_units) * 4 + (t >> 6);
       const int64_t tok = w / pieces, col = (w % pieces) * 1024 + (t & 63) * 16;
       if (tok >= p.T || col >= p.D) continue;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(p.q + tok * p.ld_q + col);
+      const u32x4 v = load_vec<kReadOnce, u32x4>(p.q + tok * p.ld_q + col);
       for (int j = 0; j < int(p.k); ++j) {
         const int row = p.row_of_slot[tok * p.k + j];
         if (row >= 0) *reinterpret_cast<u32x4*>(p.a + row * p.ld_a + col) = v;
@@ -247,14 +263,10 @@ hipError_t launch_moe_dispatch(const DispatchArgs& p, hipStream_t st) {
     hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(1024), 0, st, p, int((slots + 1023) / 1024 * 64), bits);
   } else {
     const int64_t chunk = dispatch_chunk(slots);
-    const dim3 grid(unsigned((chunks + 3) / 4));
-    hipLaunchKernelGGL(plan_count_kernel, grid, dim3(256), 0, st, p, chunk, chunks);
-    hipError_t e = hipGetLastError();
+    hipLaunchKernelGGL(plan_count_kernel, dim3(unsigned((chunks + 3) / 4)), dim3(256), 0, st, p, chunk, chunks);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(plan_scan_kernel, dim3(1), dim3(1024), 0, st, p, int(chunks), bits);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(plan_place_kernel, grid, dim3(256), 0, st, p, chunk, chunks, bits);
+    hipLaunchKernelGGL(plan_place_kernel, dim3(unsigned((chunks + 15) / 16)), dim3(1024), 0, st, p, chunk, int(chunks), bits);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.T == 0 || p.D == 0) return e;

@@ -42,15 +42,14 @@ hipError_t launch_rmsnorm_backward(const NormBwdArgs& p, bool x_bf16, bool w_bf1
 // The widest row that a workgroup keeps in registers.
 constexpr int64_t kMaxNormD = 32768;
 
-// Threads that share a row, and rows that a workgroup of them has in hand.
-inline int norm_bwd_threads(int64_t D) { return D <= 1024 ? 64 : D <= 8192 ? 256 : 1024; }
-
-// Workgroups of the gradient kernel, each of which leaves one partial sum of
-// dw per column.
+// Rows that a workgroup of the gradient kernel has in hand (a wave each up to
+// 1024 channels), and workgroups, each of which leaves one partial sum of dw per
+// column.  Beyond 256 of them a workgroup takes two rows before there are more:
+// the second kernel reads every part.
 inline int64_t norm_bwd_parts(int64_t M, int64_t D) {
-  const int64_t rows = norm_bwd_threads(D) == 64 ? 4 : 1, want = (M + rows - 1) / rows;
-  const int64_t most = norm_bwd_threads(D) == 1024 ? 256 : 512;
-  return want < most ? want : most;
+  const int64_t rows = D <= 1024 ? 4 : 1, want = (M + rows - 1) / rows, most = D <= 4096 ? 512 : 256;
+  const int64_t parts = want <= 256 ? want : (want + 1) / 2 > 256 ? (want + 1) / 2 : 256;
+  return parts < most ? parts : most;
 }
 inline int64_t norm_bwd_workspace(int64_t M, int64_t D) { return norm_bwd_parts(M, D) * ((D + 7) / 8 * 8) * 4; }
 
@@ -79,13 +78,12 @@ struct RouteBwdArgs {
 };
 hipError_t launch_moe_route_backward(const RouteBwdArgs& p, bool bf16, hipStream_t st);
 
-// Tokens that a workgroup has in hand.
-inline int64_t route_tokens(int64_t E) { return E <= 64 ? 32 : E <= 128 ? 16 : E <= 256 ? 8 : 4; }
-
-// Workgroups of the forward kernel.  One alone finishes the sums itself.
+// Workgroups of the forward kernel.  Up to 64 tokens (of 64 experts; 8 of 1024)
+// one of 256 threads does it all; otherwise they have 1024 threads.
+inline int64_t route_lanes(int64_t E) { return E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ? 32 : 64; }
 inline int64_t route_parts(int64_t T, int64_t E) {
-  const int64_t turns = (T + route_tokens(E) - 1) / route_tokens(E);
-  return turns <= 2 ? 1 : turns < 512 ? turns : 512;
+  const int64_t few = 2 * 256 / route_lanes(E), turns = (T * route_lanes(E) + 1023) / 1024;
+  return T <= few ? 1 : turns < 2 ? 2 : turns < 512 ? turns : 512;
 }
 // Sums of p, counts, tokens, and the loss's shares of up to 16 workgroups.
 inline int64_t route_workspace(int64_t T, int64_t E) {

@@ -46,18 +46,23 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(NormArgs
   // the last rows' threads stay for the barriers (TPR > 64) and lane exchanges of the others
   for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < p.M; row0 += int64_t(gridDim.x) * RPB) {
     const int64_t row = row0 + threadIdx.x / TPR;
-    const int64_t D = row < p.M ? p.D : 0;
+    const int D = row < p.M ? int(p.D) : 0;
     Row8<T> xr[R], rr[R];
     Row8<W> wr[R];
+    if (r || OUT != kOutNone) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) load_raw(xr[i], x + row * p.ld_x, int64_t(i * TPR + t) * 8, D);
+      for (int i = 0; i < R; ++i) load_raw<kReadOnce>(xr[i], x + row * p.ld_x, (i * TPR + t) * 8, D);
+    } else {                                       // the second pass over both tilings reads x again
+#pragma unroll
+      for (int i = 0; i < R; ++i) load_raw(xr[i], x + row * p.ld_x, (i * TPR + t) * 8, D);
+    }
     if (r) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) load_raw(rr[i], r + row * p.ld_r, int64_t(i * TPR + t) * 8, D);
+      for (int i = 0; i < R; ++i) load_raw<kReadOnce>(rr[i], r + row * p.ld_r, (i * TPR + t) * 8, D);
     }
     if constexpr (OUT != kOutNone) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) load_raw(wr[i], weight, int64_t(i * TPR + t) * 8, D);
+      for (int i = 0; i < R; ++i) load_raw(wr[i], weight, (i * TPR + t) * 8, D);
     }
     float v[R][8], sum = 0.0f;
 #pragma unroll
@@ -67,7 +72,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(NormArgs
       if (r) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] += rr[i].get(j);
-        store_raw(h + row * p.ld_h, int64_t(i * TPR + t) * 8, D, v[i]);
+        store_raw(h + row * p.ld_h, (i * TPR + t) * 8, D, v[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = held(v[i][j], T());
       }
@@ -83,18 +88,18 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(NormArgs
       for (int i = 0; i < R; ++i) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * wr[i].get(j);
-        if (y) store_raw(y + row * p.ld_y, int64_t(i * TPR + t) * 8, D, v[i]);
+        if (y) store_raw(y + row * p.ld_y, (i * TPR + t) * 8, D, v[i]);
         const float a = max_abs8(v[i]);
         if constexpr (OUT == kOutInt8) {
           row_a = __builtin_fmaxf(row_a, a);
         } else {
           constexpr int MODE = OUT == kOutFp8Pow2 ? kModePow2 : kModeMaxAbs;
           const ScalePair sp = scale_from_amax_bits<MODE>(row16_max_u32(__float_as_uint(a)));
-          const int64_t col = int64_t(i * TPR + t) * 8;
+          const int col = (i * TPR + t) * 8;
           if (col < D) {
             *reinterpret_cast<uint2*>(p.q + row * p.ld_q + col) =
                 uint2{quant4(v[i][0], v[i][1], v[i][2], v[i][3], sp.inv), quant4(v[i][4], v[i][5], v[i][6], v[i][7], sp.inv)};
-            if ((t & 15) == 0) p.scales[(col >> 7) * p.M + row] = sp.s;
+            if ((t & 15) == 0) p.scales[int64_t(col >> 7) * p.M + row] = sp.s;
           }
         }
       }
@@ -104,7 +109,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(NormArgs
         if (t == 0 && row < p.M) p.scales[row] = a * (1.0f / 127.0f);
         int8_t* q = reinterpret_cast<int8_t*>(p.q) + row * p.ld_q;
 #pragma unroll
-        for (int i = 0; i < R; ++i) store_run(q, int64_t(i * TPR + t) * 8, D, v[i], inv);
+        for (int i = 0; i < R; ++i) store_run(q, (i * TPR + t) * 8, D, v[i], inv);
       }
     }
     if constexpr (TPR > 64) __syncthreads();       // `part` is reused by the next row
@@ -133,7 +138,10 @@ __global__ __launch_bounds__(512) void rmsnorm_dual_kernel(NormArgs p) {
   const int t = threadIdx.x, c16 = t & 15, rq = t >> 4;
   const int64_t cblocks = p.D >> 7, rblocks = (p.M + 127) >> 7, mp = rblocks << 7;
   for (int64_t u = blockIdx.x; u < cblocks * rblocks; u += gridDim.x) {   // block-uniform: barriers stay matched
-    const int64_t br = u % rblocks, bc = u / rblocks;
+    // Backwards, four row blocks at a time: what the kernel before wrote last is still in the caches, and the four
+    // extend the same 512 bytes of q_t.
+    const int64_t left = rblocks - u / (4 * cblocks) * 4, high = left < 4 ? left : 4, v4 = u % (4 * cblocks);
+    const int64_t br = left - 1 - v4 % high, bc = v4 / high;
     const int64_t col = bc * 128 + c16 * 8, row0 = br * 128 + rq * 4;
     Row8<T> hr[4];
     Row8<W> wr;

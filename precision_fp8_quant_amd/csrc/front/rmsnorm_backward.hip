@@ -17,7 +17,9 @@ namespace {
 template <typename T, typename W, int TPR, int R>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel(NormBwdArgs p) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
-  __shared__ float part[NT / 64];
+  // With four runs the registers hold no more than dy, h and the sums of dw.
+  constexpr bool LATE = R > 2;
+  __shared__ float part[2][NT / 64];
   const int t = threadIdx.x & (TPR - 1);
   const T* __restrict__ dy = static_cast<const T*>(p.dy);
   const T* __restrict__ h = static_cast<const T*>(p.h);
@@ -29,45 +31,56 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
   float acc[R][8];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    load_raw(wr[i], weight, int64_t(i * TPR + t) * 8, p.D);
+    if constexpr (!LATE) load_raw(wr[i], weight, (i * TPR + t) * 8, int(p.D));
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
   }
+  int odd = 0;
   // the last rows' threads stay for the barriers (TPR > 64) and lane exchanges of the others
   for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < p.M; row0 += int64_t(gridDim.x) * RPB) {
     const int64_t row = row0 + threadIdx.x / TPR;
-    const int64_t D = row < p.M ? p.D : 0;
+    const int D = row < p.M ? int(p.D) : 0;
     Row8<T> yr[R], hr[R], er[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) load_raw(yr[i], dy + row * p.ld_dy, int64_t(i * TPR + t) * 8, D);
+    for (int i = 0; i < R; ++i) load_raw<kReadOnce>(yr[i], dy + row * p.ld_dy, (i * TPR + t) * 8, D);
 #pragma unroll
-    for (int i = 0; i < R; ++i) load_raw(hr[i], h + row * p.ld_h, int64_t(i * TPR + t) * 8, D);
-    if (dh) {
+    for (int i = 0; i < R; ++i) load_raw<kReadOnce>(hr[i], h + row * p.ld_h, (i * TPR + t) * 8, D);
+    if (!LATE && dh) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) load_raw(er[i], dh + row * p.ld_dh, int64_t(i * TPR + t) * 8, D);
+      for (int i = 0; i < R; ++i) load_raw<kReadOnce>(er[i], dh + row * p.ld_dh, (i * TPR + t) * 8, D);
     }
     const float rs = row < p.M ? p.rstd[row] : 0.0f;
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i) {
+      if constexpr (LATE) load_raw(wr[i], weight, (i * TPR + t) * 8, D);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float z = yr[i].get(j) * (hr[i].get(j) * rs);
         acc[i][j] += z;
         sum = __builtin_fmaf(z, wr[i].get(j), sum);
       }
-    const float c = row_sum<TPR>(sum, part) * inv_d;
+      if constexpr (LATE) asm volatile("" ::: "memory");
+    }
+    const float c = row_sum<TPR>(sum, part[odd]) * inv_d;
+    odd ^= 1;                                      // the next row's sums go to the other half: one barrier a row
 #pragma unroll
     for (int i = 0; i < R; ++i) {
+      yr[i].opaque();                              // unpacked again rather than held unpacked
+      hr[i].opaque();
+      if constexpr (LATE) {
+        load_raw(wr[i], weight, (i * TPR + t) * 8, D);
+        if (dh) load_raw<kReadOnce>(er[i], dh + row * p.ld_dh, (i * TPR + t) * 8, D);
+      }
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v[j] = rs * __builtin_fmaf(-(hr[i].get(j) * rs), c, yr[i].get(j) * wr[i].get(j));
         if (dh) v[j] += er[i].get(j);
       }
-      store_raw(dx + row * p.ld_dx, int64_t(i * TPR + t) * 8, D, v);
+      store_raw(dx + row * p.ld_dx, (i * TPR + t) * 8, D, v);
+      if constexpr (LATE) asm volatile("" ::: "memory");
     }
-    if constexpr (TPR > 64) __syncthreads();       // `part` is reused by the next row
   }
   const int64_t dp = (p.D + 7) / 8 * 8;
   float* out = p.part + int64_t(blockIdx.x) * dp;
@@ -128,8 +141,8 @@ hipError_t launch(const NormBwdArgs& p, hipStream_t st) {
     if (p.D <= 512) launch_rows<T, W, 64, 1>(p, parts, st);
     else if (p.D <= 1024) launch_rows<T, W, 64, 2>(p, parts, st);
     else if (p.D <= 2048) launch_rows<T, W, 256, 1>(p, parts, st);
-    else if (p.D <= 4096) launch_rows<T, W, 256, 2>(p, parts, st);
-    else if (p.D <= 8192) launch_rows<T, W, 256, 4>(p, parts, st);
+    else if (p.D <= 4096) launch_rows<T, W, 512, 1>(p, parts, st);
+    else if (p.D <= 8192) launch_rows<T, W, 1024, 1>(p, parts, st);
     else if (p.D <= 16384) launch_rows<T, W, 1024, 2>(p, parts, st);
     else launch_rows<T, W, 1024, 4>(p, parts, st);
     const hipError_t e = hipGetLastError();

@@ -10,9 +10,9 @@
 // equal.
 //
 // A lane has the same 8 C experts in all of its workgroup's tokens and sums
-// their p in registers; workgroups leave one row of sums and counts each, which
-// a second kernel adds in a fixed order.  With one workgroup it is all one
-// launch.
+// their p in registers, a wave its groups', a workgroup its waves'; workgroups
+// leave one row of sums and counts each, which a second kernel adds in a fixed
+// order.  With one workgroup it is all one launch.
 #include "front_launch.h"
 #include "lanes.h"
 #include "row_io.h"
@@ -69,19 +69,34 @@ __device__ __forceinline__ float slope_of(int64_t E, int64_t k, int count, int t
   return tokens > 0 ? float(E) * float(count) / (float(k) * float(tokens) * float(tokens)) : 0.0f;
 }
 
-template <typename T, int LPT, int C>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
-  constexpr int G = 256 / LPT;                     // tokens at a time
+// v summed over the lanes that have the same place in their group of LPT.
+template <int LPT>
+__device__ __forceinline__ float groups_sum(float v) {
+  if constexpr (LPT <= 8) v += __uint_as_float(dpp<0x128>(__float_as_uint(v)));        // row_ror by 8: the other half row
+  if constexpr (LPT <= 16) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(uint32_t(a[0])) + __uint_as_float(uint32_t(a[1]));
+  }
+  if constexpr (LPT <= 32) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(uint32_t(a[0])) + __uint_as_float(uint32_t(a[1]));
+  }
+  return v;
+}
+
+template <typename T, int LPT, int C, int NT>
+__global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
+  constexpr int G = NT / LPT;                      // tokens at a time
   constexpr int EP = C * LPT * 8;                  // experts with room
   constexpr int ROUNDS = (kMaxChosen + LPT - 1) / LPT;
-  __shared__ float sums[G][EP];
+  __shared__ float sums[NT / 64][EP];
   __shared__ int chosen[EP];
   __shared__ int tokens;
-  __shared__ float part[4];
+  __shared__ float part[NT / 64];
   const int lane = threadIdx.x & (LPT - 1), group = threadIdx.x / LPT;
   const T* __restrict__ logits = static_cast<const T*>(p.logits);
   const int E = int(p.E), k = int(p.k);
-  for (int e = threadIdx.x; e < EP; e += 256) chosen[e] = 0;
+  for (int e = threadIdx.x; e < EP; e += NT) chosen[e] = 0;
   if (threadIdx.x == 0) tokens = 0;
   __syncthreads();
   float acc[C][8];
@@ -152,13 +167,17 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sums[group][(c * LPT + lane) * 8 + j] = acc[c][j];
+    for (int j = 0; j < 8; ++j) {
+      const float s = groups_sum<LPT>(acc[c][j]);
+      if ((threadIdx.x & 63) < LPT) sums[threadIdx.x >> 6][(c * LPT + lane) * 8 + j] = s;
+    }
   __syncthreads();
   const bool alone = gridDim.x == 1;
   float loss = 0.0f;
-  for (int e = threadIdx.x; e < E; e += 256) {
+  for (int e = threadIdx.x; e < E; e += NT) {
     float s = sums[0][e];
-    for (int g = 1; g < G; ++g) s += sums[g][e];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) s += sums[w][e];
     if (alone) {
       const float slope = slope_of(p.E, p.k, chosen[e], tokens);
       p.counts[e] = chosen[e];
@@ -170,7 +189,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
     }
   }
   if (alone) {
-    loss = row_sum<256>(loss, part);
+    loss = row_sum<NT>(loss, part);
     if (threadIdx.x == 0) p.loss[0] = loss;
   } else if (threadIdx.x == 0) {
     p.part_n[blockIdx.x] = tokens;
@@ -325,7 +344,8 @@ template <typename T>
 hipError_t launch_route_t(const RouteArgs& p, hipStream_t st) {
   const int64_t parts = route_parts(p.T, p.E);
   const hipError_t e = by_experts(p.E, [&](auto lpt, auto c) {
-    hipLaunchKernelGGL((route_kernel<T, lpt(), c()>), dim3(unsigned(parts)), dim3(256), 0, st, p);
+    if (parts == 1) hipLaunchKernelGGL((route_kernel<T, lpt(), c(), 256>), dim3(1), dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((route_kernel<T, lpt(), c(), 1024>), dim3(unsigned(parts)), dim3(1024), 0, st, p);
     return hipGetLastError();
   });
   if (e != hipSuccess || parts == 1) return e;

@@ -6,25 +6,41 @@
 
 namespace fp8q {
 
-__device__ __forceinline__ void put1(Row8<uint16_t>& x, int i, const uint16_t* p) {
-  x.w[i >> 1] |= uint32_t(*p) << (16 * (i & 1));
+// The first n of the eight, zeros in place of the others.
+__device__ __forceinline__ void keep(Row8<uint16_t>& x, int n) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x.w[i] = 2 * i + 1 < n ? x.w[i] : 2 * i < n ? x.w[i] & 0xFFFFu : 0u;
 }
-__device__ __forceinline__ void put1(Row8<float>& x, int i, const float* p) {
-  if (i < 4) x.a[i] = *p;
-  else x.b[i - 4] = *p;
+__device__ __forceinline__ void keep(Row8<float>& x, int n) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x.a[i] = i < n ? x.a[i] : 0.0f;
+    x.b[i] = 4 + i < n ? x.b[i] : 0.0f;
+  }
+}
+// kReadOnce: past the caches, for what nobody reads again.
+enum Reuse { kReadAgain, kReadOnce };
+template <Reuse U, typename V>
+__device__ __forceinline__ V load_vec(const void* p) {
+  if constexpr (U == kReadOnce) return __builtin_nontemporal_load(static_cast<const V*>(p));
+  else return *static_cast<const V*>(p);
+}
+template <Reuse U>
+__device__ __forceinline__ void load_chunks(Row8<uint16_t>& x, const uint16_t* p, int) { x.w = load_vec<U, u32x4>(p); }
+template <Reuse U>
+__device__ __forceinline__ void load_chunks(Row8<float>& x, const float* p, int n) {
+  x.a = load_vec<U, v4f>(p);
+  if (n > 4) x.b = load_vec<U, v4f>(p + 4);
 }
 
-// Elements [col, col + 8) of a row of `cols`; zeros beyond its end.
-template <typename T>
-__device__ __forceinline__ void load_raw(Row8<T>& x, const T* row, int64_t col, int64_t cols) {
-  if (col + 8 <= cols) {
-    x.load(row + col);
-  } else {
-    x.zero();
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (col + i < cols) put1(x, i, row + col + i);
-  }
+// Elements [col, col + 8) of a row of `cols`; zeros beyond its end.  Rows are
+// 16-byte aligned, and the 16 bytes that an element lies in are read whole:
+// they are in one page, and what the row does not own of them is not used.
+template <Reuse U = kReadAgain, typename T>
+__device__ __forceinline__ void load_raw(Row8<T>& x, const T* row, int col, int cols) {
+  x.zero();
+  if (col < cols) load_chunks<U>(x, row + col, cols - col);
+  if (col + 8 > cols && col < cols) keep(x, cols - col);
 }
 
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = uint16_t(pack_bf16(v, 0.0f)); }
@@ -32,7 +48,7 @@ __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
 // v rounded to T, elements [col, col + 8) of a row of `cols`; nothing beyond its end.
 template <typename T>
-__device__ __forceinline__ void store_raw(T* row, int64_t col, int64_t cols, const float (&v)[8]) {
+__device__ __forceinline__ void store_raw(T* row, int col, int cols, const float (&v)[8]) {
   if (col + 8 <= cols) {
     store8(row + col, v);
   } else {

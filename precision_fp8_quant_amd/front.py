@@ -17,7 +17,7 @@ import ctypes
 import torch
 
 from . import MAXABS, _cdiv, _codes, _expect, _i64, _int, _outputs_on, _ptr, _rowmajor, lib
-from .ffn import _CODE, _call, _f32, _i8, _ld, _out
+from .ffn import _CODE, _call, _done, _f32, _i8, _ld, _native, _out
 
 _f = ctypes.c_float
 
@@ -48,6 +48,10 @@ for _name, _argtypes in {**SIGNATURES, **SIZES}.items():
     getattr(lib, _name).restype = _i64 if _name in SIZES else ctypes.c_int
 
 _i32 = torch.int32
+
+# The usual call (new outputs, current device and stream) is made by csrc/front/binding.cpp in one step; it answers None
+# for anything else, and an int where the C ABI refuses.  What follows it here takes every call, and says what is wrong
+# with one.
 
 
 def _code(t, name):
@@ -125,6 +129,11 @@ def fp8_rmsnorm(x, weight, residual=None, eps=1e-6, mode=MAXABS, transposed=Fals
     (128x1 tiles, Wgrad's operand), Mp being M rounded up to whole 128-row tiles, which q and scales then have too, the
     rows past M zero; h where there is a residual; rstd [M] with save_rstd=True, for rmsnorm_backward; y itself, in
     x's type, with save_y=True.  Giving an output's tensor asks for it."""
+    if _native and stream is None and h is None and rstd is None and y is None and q is None and scales is None and \
+            q_t is None and scales_t is None:
+        r = _native.fp8_rmsnorm(x, weight, residual, eps, mode, transposed, save_rstd, save_y)
+        if r is not None:
+            return _done(r)
     m, d, dev, code, w_code = _norm_inputs(x, weight, residual, h)
     if not transposed and (q_t is not None or scales_t is not None):
         raise ValueError("q_t / scales_t are the transposed copy: pass transposed=True")
@@ -161,6 +170,10 @@ def int8_rmsnorm(x, weight, residual=None, eps=1e-6, save_rstd=False, save_y=Fal
                  scales=None, stream=None):
     """The norm of fp8_rmsnorm in 8-bit integers with one scale for each row: q int8 [M][D], scales [M], and h, rstd and
     y as far as asked for."""
+    if _native and stream is None and h is None and rstd is None and y is None and q is None and scales is None:
+        r = _native.int8_rmsnorm(x, weight, residual, eps, save_rstd, save_y)
+        if r is not None:
+            return _done(r)
     m, d, dev, code, w_code = _norm_inputs(x, weight, residual, h)
     with _outputs_on(stream, dev, q, scales, *((h,) if residual is not None else ()), *((rstd,) if save_rstd else ()),
                      *((y,) if save_y else ())):
@@ -182,6 +195,10 @@ def int8_rmsnorm(x, weight, residual=None, eps=1e-6, save_rstd=False, save_y=Fal
 def rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dw=None, accumulate=False, stream=None):
     """Gradient of the norm y = h rstd weight: dx [M][D] of h (of x and of the residual alike), with dh, the gradient that
     reaches h past the norm, added, and dw FP32 [D] of the weight, added to dw with accumulate=True."""
+    if _native and stream is None and dx is None and dw is None and not accumulate:
+        r = _native.rmsnorm_backward(dy, h, weight, rstd, dh)
+        if r is not None:
+            return _done(r)
     _rowmajor(dy, "dy")
     (m, d), dev, code = dy.shape, dy.device, _code(dy, "dy")
     _expect(h, "h", dy.dtype, (m, d), dev)
@@ -209,6 +226,11 @@ def moe_route(logits, k, valid=None, renormalize=False, weights=None, experts=No
     renormalize=True), experts int32 [T][k] in descending order, counts int32 [E], loss FP32 [1], the balance loss
     E sum_e f_e P_e, and slope FP32 [E], its gradient by each token's probabilities.  valid (bool or uint8 [T]) says
     which tokens count; the others have experts -1.  A logit of minus infinity is never chosen."""
+    if _native and stream is None and weights is None and experts is None and counts is None and loss is None and \
+            slope is None:
+        r = _native.moe_route(logits, k, valid, renormalize)
+        if r is not None:
+            return _done(r)
     _rowmajor(logits, "logits")
     (t, e), dev, code, k = logits.shape, logits.device, _code(logits, "logits"), int(k)
     if valid is not None:
@@ -229,6 +251,10 @@ def moe_route_backward(logits, experts, slope=None, dweights=None, dloss=None, r
                        stream=None):
     """Gradient of moe_route's weights and loss with respect to the logits, in their type, from dweights FP32 [T][k]
     and dloss FP32 [1] (either may be None: zero); experts and slope as moe_route left them."""
+    if _native and stream is None and dlogits is None:
+        r = _native.moe_route_backward(logits, experts, slope, dweights, dloss, renormalize)
+        if r is not None:
+            return _done(r)
     _rowmajor(logits, "logits")
     (t, e), dev, code = logits.shape, logits.device, _code(logits, "logits")
     if experts.dim() != 2:
@@ -263,6 +289,10 @@ def fp8_moe_dispatch(experts, q, scales, num_experts, a=None, a_scales=None, gro
     tiles.  a [M][D], a_scales [D/128][M], group_of_mtile int32 [M/128] (-1: tile not in use, whose rows and scales are
     left as they are), row_of_slot int32 [T][k] (-1 for experts outside the range), token_of_row int32 [M] (-1: none).
     M is moe_max_rows(T, k, E), or what the first given one of a, a_scales, group_of_mtile and token_of_row has."""
+    if _native and stream is None and group_of_mtile is None and row_of_slot is None and token_of_row is None:
+        r = _native.fp8_moe_dispatch(experts, q, scales, num_experts, a, a_scales)
+        if r is not None:
+            return _done(r)
     q = _codes(_rowmajor(q, "q"))
     (t, d), dev, e = q.shape, q.device, int(num_experts)
     if experts.dim() != 2:
