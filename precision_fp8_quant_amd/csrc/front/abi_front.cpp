@@ -50,6 +50,12 @@ int check_norm(const fp8q::NormArgs& p, int64_t xs) {
   return FP8Q_OK;
 }
 
+// Whether n inputs of M x D are more than the caches are good for.  D is at most
+// kMaxNormD where it matters.
+bool read_once(int64_t M, int64_t D, int64_t es, int64_t n) {
+  return D > 0 && M > fp8q::kReadOnceBytes / (es * n) / D;
+}
+
 bool eps_ok(float eps) { return eps > 0.0f && eps <= 3.4028234664e38f; }   // false for NaN
 
 bool route_sizes_ok(int64_t T, int64_t E, int64_t k, int64_t most) {
@@ -70,7 +76,7 @@ int fp8_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_r,
   if (M == 0 || D == 0) return FP8Q_OK;
   const int64_t xs = dtype_size(x_dtype), ws = dtype_size(w_dtype);
   const fp8q::NormArgs p{x, ld_x, residual, ld_r, M, D, weight, eps, h, ld_h, rstd, y, ld_y, q, ld_q, scales, q_t, ld_qt,
-                         scales_t};
+                         scales_t, read_once(M, D, xs, residual ? 2 : 1)};
   if (!q_t != !scales_t) return FP8Q_ERR_NULL;
   if (q_t && !rstd) return FP8Q_ERR_NULL;
   const int bad = check_norm(p, xs);
@@ -101,7 +107,8 @@ int int8_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_r
   if (M == 0) return FP8Q_OK;
   const int64_t xs = dtype_size(x_dtype), ws = dtype_size(w_dtype);
   const fp8q::NormArgs p{x, ld_x, residual, ld_r, M, D, weight, eps, h, ld_h, rstd, y, ld_y,
-                         reinterpret_cast<uint8_t*>(q), ld_q, scales, nullptr, 0, nullptr};
+                         reinterpret_cast<uint8_t*>(q), ld_q, scales, nullptr, 0, nullptr,
+                         read_once(M, D, xs, residual ? 2 : 1)};
   const int bad = check_norm(p, xs);
   if (bad != FP8Q_OK) return bad;
   const Range outs[5] = {matrix(h, M, D, ld_h, xs), packed(rstd, M, 4), matrix(y, M, D, ld_y, xs), matrix(q, M, D, ld_q, 1),
@@ -140,7 +147,7 @@ int rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h,
   const int clash = check_ranges(outs, ins);
   if (clash != FP8Q_OK) return clash;
   const fp8q::NormBwdArgs p{dy, ld_dy, h, ld_h, M, D, weight, rstd, dh, ld_dh, dx, ld_dx, dw, accumulate == 1,
-                            static_cast<float*>(workspace)};
+                            static_cast<float*>(workspace), read_once(M, D, xs, dh ? 3 : 2)};
   return from_hip(fp8q::launch_rmsnorm_backward(p, x_dtype == FP8Q_BF16, w_dtype == FP8Q_BF16,
                                                 reinterpret_cast<hipStream_t>(stream)));
 }

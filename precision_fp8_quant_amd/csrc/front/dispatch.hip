@@ -8,8 +8,9 @@
 // lane's place is the expert's running count plus its equals in lower lanes.
 //   up to 8192 slots   one workgroup: counts of its 16 waves' chunks, their
 //                      prefix sums and the tile map, the rows
-//   beyond             two kernels over up to 128 chunks: their counts; then the
-//                      rows, every workgroup summing all counts for itself
+//   beyond             two kernels of up to 128 workgroups of 16 chunks: the counts
+//                      of chunks and workgroups; then the rows, every workgroup
+//                      summing the others' counts for itself
 // Then one kernel moves codes and scales: a token's row is read once and
 // written to its k places; scales, which lie transposed, are written in runs of
 // a tile's 128 rows, with the padding rows of the tile.
@@ -22,7 +23,7 @@ namespace {
 
 constexpr uint32_t kZeroScaleBits = 0x00800000u;   // 2^-126: the scale of a row of zeros
 
-constexpr int kSteps = 8;     // steps of 64 slots whose experts a wave loads together
+constexpr int kSteps = 4;     // steps of 64 slots whose experts a wave loads together
 
 // The experts of slots [s, s + 64 kSteps) up to `end`, a lane's at s + 64 i + lane; -1 for no expert.
 __device__ __forceinline__ void load_experts(const DispatchArgs& p, int64_t s, int64_t end, int (&e)[kSteps]) {
@@ -149,45 +150,56 @@ __global__ __launch_bounds__(1024) void plan_kernel(DispatchArgs p, int chunk, i
   place_chunk(p, begin, end, bits, next[wave], first_experts);
 }
 
-__global__ __launch_bounds__(256) void plan_count_kernel(DispatchArgs p, int64_t chunk, int64_t chunks) {
-  __shared__ int count[4][kMaxExperts];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, E = int(p.E);
-  const int64_t c = int64_t(blockIdx.x) * 4 + wave;
-  for (int e = lane; e < E; e += 64) count[wave][e] = 0;
+// hist: the counts of each chunk, [chunks][E], then those of each workgroup.
+__global__ __launch_bounds__(1024) void plan_count_kernel(DispatchArgs p, int64_t chunk) {
+  __shared__ int count[16][kMaxExperts];
+  const int t = threadIdx.x, wave = t >> 6, E = int(p.E);
+  const int64_t c = int64_t(blockIdx.x) * 16 + wave, chunks = int64_t(gridDim.x) * 16;
+  for (int e = t & 63; e < E; e += 64) count[wave][e] = 0;
   __syncthreads();
-  if (c < chunks) {
-    const int64_t slots = p.T * p.k, end = (c + 1) * chunk < slots ? (c + 1) * chunk : slots;
-    count_chunk(p, c * chunk, end, count[wave]);
+  const int64_t slots = p.T * p.k, end = (c + 1) * chunk < slots ? (c + 1) * chunk : slots;
+  count_chunk(p, c * chunk, end, count[wave]);
+  __syncthreads();
+  for (int e = t & 63; e < E; e += 64) p.hist[c * E + e] = count[wave][e];
+  if (t < E) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) n += count[w][t];
+    p.hist[(chunks + blockIdx.x) * E + t] = n;
   }
-  __syncthreads();
-  if (c < chunks)
-    for (int e = lane; e < E; e += 64) p.hist[c * E + e] = count[wave][e];
 }
 
-// 16 chunks a workgroup.  Up to 16 threads (1024 over E rounded up to a power
-// of two) sum an expert's counts over consecutive pieces of the chunks: all of
-// them for the first rows of the experts, those before the workgroup's for its
-// own.  The first workgroup also writes the maps.
-__global__ __launch_bounds__(1024) void plan_place_kernel(DispatchArgs p, int64_t chunk, int chunks, int bits) {
+// Up to 16 threads (1024 over E rounded up to a power of two) sum an expert's
+// counts over consecutive pieces of the workgroups: all of them for the first
+// rows of the experts, those before this one for its own.  The first workgroup
+// also writes the maps.
+__global__ __launch_bounds__(1024) void plan_place_kernel(DispatchArgs p, int64_t chunk, int bits) {
   __shared__ int next[16][kMaxExperts];
   __shared__ int place[kMaxExperts][2];
   __shared__ int wave_sum[16];
   int* sums = next[0];                             // [2][1024], before next[] is filled
   const int t = threadIdx.x, wave = t >> 6, E = int(p.E), ep = 1 << bits, share = bits < 6 ? 16 : 1024 >> bits;
-  const int mine = blockIdx.x * 16, c = mine + wave;
-  const int64_t slots = p.T * p.k, begin = c * chunk, end = begin + chunk < slots ? begin + chunk : slots;
+  const int blocks = gridDim.x, mine = blockIdx.x;
+  const int64_t c = int64_t(mine) * 16 + wave, slots = p.T * p.k, begin = c * chunk;
+  const int64_t end = begin + chunk < slots ? begin + chunk : slots;
+  const int* group_counts = p.hist + int64_t(blocks) * 16 * E;
   int experts[kSteps];
   load_experts(p, begin, end, experts);
-  const int e = t & (ep - 1), piece = t >> bits, len = (chunks + share - 1) / share;
-  const int c0 = piece * len, c1 = c0 + len < chunks ? c0 + len : chunks;
+  const int e = t & (ep - 1), piece = t >> bits, len = (blocks + share - 1) / share;
+  const int c0 = piece * len, c1 = c0 + len < blocks ? c0 + len : blocks;
   int all = 0, before = 0;
   if (e < E && piece < share) {
-#pragma unroll 8
+#pragma unroll 4
     for (int i = c0; i < c1; ++i) {
-      const int n = p.hist[int64_t(i) * E + e];
+      const int n = group_counts[int64_t(i) * E + e];
       all += n;
       before += i < mine ? n : 0;
     }
+  }
+  int own[16];
+  if (t < E) {
+#pragma unroll
+    for (int w = 0; w < 16; ++w) own[w] = p.hist[(int64_t(mine) * 16 + w) * E + t];
   }
   sums[t] = all;
   sums[1024 + t] = before;
@@ -205,7 +217,7 @@ __global__ __launch_bounds__(1024) void plan_place_kernel(DispatchArgs p, int64_
 #pragma unroll
     for (int w = 0; w < 16; ++w) {
       next[w][t] = row;
-      if (mine + w < chunks) row += p.hist[int64_t(mine + w) * E + t];
+      row += own[w];
     }
   }
   if (blockIdx.x == 0) write_maps(p, all, first, used, place);
@@ -239,7 +251,7 @@ __global__ __launch_bounds__(256) void move_kernel(DispatchArgs p, int64_t tile_
       const int64_t pieces = (p.D + 1023) >> 10, w = (u - tile_units) * 4 + (t >> 6);
       const int64_t tok = w / pieces, col = (w % pieces) * 1024 + (t & 63) * 16;
       if (tok >= p.T || col >= p.D) continue;
-      const u32x4 v = load_vec<kReadOnce, u32x4>(p.q + tok * p.ld_q + col);
+      const u32x4 v = load_vec<true, u32x4>(p.q + tok * p.ld_q + col);
       for (int j = 0; j < int(p.k); ++j) {
         const int row = p.row_of_slot[tok * p.k + j];
         if (row >= 0) *reinterpret_cast<u32x4*>(p.a + row * p.ld_a + col) = v;
@@ -257,16 +269,17 @@ int bits_of(int64_t E) {                           // bits that tell E experts a
 }  // namespace
 
 hipError_t launch_moe_dispatch(const DispatchArgs& p, hipStream_t st) {
-  const int64_t slots = p.T * p.k, chunks = dispatch_chunks(slots);
+  const int64_t slots = p.T * p.k;
+  const unsigned groups = unsigned(dispatch_groups(slots));
   const int bits = bits_of(p.E);
-  if (chunks == 0) {
+  if (groups == 0) {
     hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(1024), 0, st, p, int((slots + 1023) / 1024 * 64), bits);
   } else {
     const int64_t chunk = dispatch_chunk(slots);
-    hipLaunchKernelGGL(plan_count_kernel, dim3(unsigned((chunks + 3) / 4)), dim3(256), 0, st, p, chunk, chunks);
+    hipLaunchKernelGGL(plan_count_kernel, dim3(groups), dim3(1024), 0, st, p, chunk);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(plan_place_kernel, dim3(unsigned((chunks + 15) / 16)), dim3(1024), 0, st, p, chunk, int(chunks), bits);
+    hipLaunchKernelGGL(plan_place_kernel, dim3(groups), dim3(1024), 0, st, p, chunk, bits);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.T == 0 || p.D == 0) return e;

@@ -11,6 +11,14 @@
 
 namespace fp8q {
 
+// Inputs beyond this many bytes are read past the caches, of which the largest
+// holds 256 MB: what is read once would only push out what is read again.
+// Smaller ones may still be there from the kernel that wrote them.  Measured (us,
+// past the caches / through them): norm of 8192x7168 BF16 with a residual, 235
+// MB, inputs just written 78 / 88, from memory 73 / 91; 2048x7168, 59 MB, just
+// written 24.2 / 23.4, three sets in turn 28.9 / 22.9.
+constexpr int64_t kReadOnceBytes = 96 << 20;
+
 struct NormArgs {
   const void* x; int64_t ld_x;
   const void* r; int64_t ld_r;    // or nullptr
@@ -22,6 +30,7 @@ struct NormArgs {
   void* y; int64_t ld_y;          // or nullptr
   uint8_t* q; int64_t ld_q; float* scales;
   uint8_t* q_t; int64_t ld_qt; float* scales_t;   // or nullptr
+  bool once;                      // inputs past the caches
 };
 hipError_t launch_fp8_rmsnorm(const NormArgs& p, bool x_bf16, bool w_bf16, int mode, hipStream_t st);
 hipError_t launch_int8_rmsnorm(const NormArgs& p, bool x_bf16, bool w_bf16, hipStream_t st);
@@ -36,6 +45,7 @@ struct NormBwdArgs {
   void* dx; int64_t ld_dx;
   float* dw; bool accumulate;
   float* part;                    // [norm_bwd_parts(M, D)][D rounded up to 8]
+  bool once;                      // inputs past the caches
 };
 hipError_t launch_rmsnorm_backward(const NormBwdArgs& p, bool x_bf16, bool w_bf16, hipStream_t st);
 
@@ -100,22 +110,22 @@ struct DispatchArgs {
   int64_t D, M_total;
   uint8_t* a; int64_t ld_a; float* a_scales;
   int32_t* group_of_mtile; int32_t* row_of_slot; int32_t* token_of_row;
-  int32_t* hist;                  // [dispatch_chunks(T k)][E], or nullptr with one chunk
+  int32_t* hist;                  // 17 dispatch_groups(T k) rows of E, or nullptr
 };
 hipError_t launch_moe_dispatch(const DispatchArgs& p, hipStream_t st);
 
 // Slots whose ranks one workgroup alone finds.
 constexpr int64_t kDispatchAlone = 8192;
 
-// Slots of one wave, whole steps of 64, of which up to 128 waves share the rest.
+// Slots of one wave, whole steps of 64, for up to 128 workgroups of 16 waves.
 inline int64_t dispatch_chunk(int64_t slots) {
-  const int64_t steps = (slots + 64 * 128 - 1) / (64 * 128);
-  return 64 * (steps > 4 ? steps : 4);
+  const int64_t steps = (slots + 64 * 16 * 128 - 1) / (64 * 16 * 128);
+  return 64 * (steps > 2 ? steps : 2);
 }
-inline int64_t dispatch_chunks(int64_t slots) {
-  return slots <= kDispatchAlone ? 0 : (slots - 1) / dispatch_chunk(slots) + 1;
+inline int64_t dispatch_groups(int64_t slots) {
+  return slots <= kDispatchAlone ? 0 : (slots - 1) / (16 * dispatch_chunk(slots)) + 1;
 }
-inline int64_t dispatch_workspace(int64_t slots, int64_t E) { return dispatch_chunks(slots) * E * 4; }
+inline int64_t dispatch_workspace(int64_t slots, int64_t E) { return dispatch_groups(slots) * 17 * E * 4; }
 
 // Whole 128-row tiles that the slots take at most: each of n experts wastes up to 127 rows.
 inline int64_t dispatch_max_rows(int64_t slots, int64_t E) {

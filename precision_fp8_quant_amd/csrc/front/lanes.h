@@ -42,6 +42,9 @@ template <int N> __device__ __forceinline__ float lanes_max(float v) {
     return __float_as_uint(__builtin_fmaxf(__uint_as_float(a), __uint_as_float(b)));
   }));
 }
+template <int N> __device__ __forceinline__ uint32_t lanes_max_u32(uint32_t v) {
+  return lanes_reduce<N>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
 template <int N> __device__ __forceinline__ uint32_t lanes_min_u32(uint32_t v) {
   return lanes_reduce<N>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }

@@ -32,7 +32,8 @@ __device__ __forceinline__ float max_abs8(const float (&v)[8]) {
   return m;
 }
 
-template <typename T, typename W, int TPR, int R, int OUT>
+// ONCE: x and the residual past the caches.
+template <typename T, typename W, int TPR, int R, int OUT, bool ONCE>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(NormArgs p) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
   __shared__ float part[2][NT / 64];
@@ -49,16 +50,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(NormArgs
     const int D = row < p.M ? int(p.D) : 0;
     Row8<T> xr[R], rr[R];
     Row8<W> wr[R];
-    if (r || OUT != kOutNone) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) load_raw<kReadOnce>(xr[i], x + row * p.ld_x, (i * TPR + t) * 8, D);
-    } else {                                       // the second pass over both tilings reads x again
-#pragma unroll
-      for (int i = 0; i < R; ++i) load_raw(xr[i], x + row * p.ld_x, (i * TPR + t) * 8, D);
-    }
+    for (int i = 0; i < R; ++i) load_raw<ONCE>(xr[i], x + row * p.ld_x, (i * TPR + t) * 8, D);
     if (r) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) load_raw<kReadOnce>(rr[i], r + row * p.ld_r, (i * TPR + t) * 8, D);
+      for (int i = 0; i < R; ++i) load_raw<ONCE>(rr[i], r + row * p.ld_r, (i * TPR + t) * 8, D);
     }
     if constexpr (OUT != kOutNone) {
 #pragma unroll
@@ -209,7 +205,10 @@ __global__ __launch_bounds__(512) void rmsnorm_dual_kernel(NormArgs p) {
 template <typename T, typename W, int TPR, int R, int OUT>
 hipError_t launch_rows(const NormArgs& p, hipStream_t st) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
-  hipLaunchKernelGGL((rmsnorm_kernel<T, W, TPR, R, OUT>), dim3(grid_of((p.M - 1) / RPB + 1, NT)), dim3(NT), 0, st, p);
+  const dim3 grid(grid_of((p.M - 1) / RPB + 1, NT));
+  // The second pass over both tilings reads h again, which is x where there is no residual.
+  if (p.once && (p.r || OUT != kOutNone)) hipLaunchKernelGGL((rmsnorm_kernel<T, W, TPR, R, OUT, true>), grid, dim3(NT), 0, st, p);
+  else hipLaunchKernelGGL((rmsnorm_kernel<T, W, TPR, R, OUT, false>), grid, dim3(NT), 0, st, p);
   return hipGetLastError();
 }
 

@@ -14,7 +14,8 @@
 namespace fp8q {
 namespace {
 
-template <typename T, typename W, int TPR, int R>
+// ONCE: dy, h and dh past the caches.
+template <typename T, typename W, int TPR, int R, bool ONCE>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel(NormBwdArgs p) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
   // With four runs the registers hold no more than dy, h and the sums of dw.
@@ -42,12 +43,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
     const int D = row < p.M ? int(p.D) : 0;
     Row8<T> yr[R], hr[R], er[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) load_raw<kReadOnce>(yr[i], dy + row * p.ld_dy, (i * TPR + t) * 8, D);
+    for (int i = 0; i < R; ++i) load_raw<ONCE>(yr[i], dy + row * p.ld_dy, (i * TPR + t) * 8, D);
 #pragma unroll
-    for (int i = 0; i < R; ++i) load_raw<kReadOnce>(hr[i], h + row * p.ld_h, (i * TPR + t) * 8, D);
+    for (int i = 0; i < R; ++i) load_raw<ONCE>(hr[i], h + row * p.ld_h, (i * TPR + t) * 8, D);
     if (!LATE && dh) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) load_raw<kReadOnce>(er[i], dh + row * p.ld_dh, (i * TPR + t) * 8, D);
+      for (int i = 0; i < R; ++i) load_raw<ONCE>(er[i], dh + row * p.ld_dh, (i * TPR + t) * 8, D);
     }
     const float rs = row < p.M ? p.rstd[row] : 0.0f;
     float sum = 0.0f;
@@ -70,7 +71,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
       hr[i].opaque();
       if constexpr (LATE) {
         load_raw(wr[i], weight, (i * TPR + t) * 8, D);
-        if (dh) load_raw<kReadOnce>(er[i], dh + row * p.ld_dh, (i * TPR + t) * 8, D);
+        if (dh) load_raw<ONCE>(er[i], dh + row * p.ld_dh, (i * TPR + t) * 8, D);
       }
       float v[8];
 #pragma unroll
@@ -131,7 +132,8 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restri
 template <typename T, typename W, int TPR, int R>
 void launch_rows(const NormBwdArgs& p, int64_t parts, hipStream_t st) {
   constexpr int NT = TPR < 256 ? 256 : TPR;
-  hipLaunchKernelGGL((rmsnorm_backward_kernel<T, W, TPR, R>), dim3(unsigned(parts)), dim3(NT), 0, st, p);
+  if (p.once) hipLaunchKernelGGL((rmsnorm_backward_kernel<T, W, TPR, R, true>), dim3(unsigned(parts)), dim3(NT), 0, st, p);
+  else hipLaunchKernelGGL((rmsnorm_backward_kernel<T, W, TPR, R, false>), dim3(unsigned(parts)), dim3(NT), 0, st, p);
 }
 
 template <typename T, typename W>

@@ -5,9 +5,10 @@
 //   dz = p (dp - sum p dp),  dp_e = dloss slope_e + [e chosen] dc
 // LPT lanes share a token and hold its logits in registers, C runs of 8 each
 // (expert (c LPT + lane) 8 + j): one read of the logits serves the softmax and
-// the choice.  The choice is k rounds of a maximum over the lanes and of the
-// lowest index that has it, on the logits themselves, so that equal logits are
-// equal.
+// the choice.  The choice goes by the logits themselves, as integers of the same
+// order, so that equal logits are equal: every lane sorts its runs, and each of
+// the k rounds takes the largest of their heads over the lanes, the lowest index
+// where several are, and moves that run up.
 //
 // A lane has the same 8 C experts in all of its workgroup's tokens and sums
 // their p in registers, a wave its groups', a workgroup its waves'; workgroups
@@ -64,6 +65,118 @@ struct Token {
   __device__ __forceinline__ float term(float v) const { return __builtin_amdgcn_exp2f((v - m) * kLog2e); }
 };
 
+// Integer of the same order as v; both zeros are the same.  0: v is minus
+// infinity or no number.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return v > __uint_as_float(kNegInf) ? u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u) : 0u;
+}
+// The logit of a candidate's key; BF16 keys have the expert in their low half.
+__device__ __forceinline__ float logit_of(uint32_t o, float) {
+  return __uint_as_float(int32_t(o) < 0 ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ float logit_of(uint32_t o, uint16_t) {
+  return __uint_as_float((int32_t(o) < 0 ? o ^ 0x80000000u : ~o) & 0xFFFF0000u);
+}
+
+// The larger to the front.
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = a > b ? a : b;
+  b = a > b ? b : a;
+  a = hi;
+}
+
+// A lane's run of eight candidates, experts e0 .. e0 + 7, in descending order.
+// BF16 leaves room for the index below the logit: a candidate is one integer, no
+// two are equal and a round is one maximum.
+template <typename T> struct Run;
+template <> struct Run<uint16_t> {
+  uint32_t key[8];                // the logit in the high half, 0xFFFF - expert in the low one; 0: none
+  __device__ __forceinline__ void sort(const float (&z)[8], int e0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t o = ordered(z[j]);
+      key[j] = o ? (o & 0xFFFF0000u) | uint32_t(0xFFFF - (e0 + j)) : 0u;
+    }
+    constexpr int net[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                                {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+    for (int i = 0; i < 19; ++i) exchange(key[net[i][0]], key[net[i][1]]);   // odd-even merge sort
+  }
+  __device__ __forceinline__ void up(bool taken) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j) key[j] = taken ? key[j + 1] : key[j];
+    key[7] = taken ? 0u : key[7];
+  }
+};
+// FP32: logits, and their places in the run 4 bits each.  Neighbours that are
+// equal stay as they are, so that equal logits stay in the order of their index.
+template <> struct Run<float> {
+  uint32_t key[8];                // 0: none
+  uint32_t places;
+  __device__ __forceinline__ void sort(const float (&z)[8], int) {
+    uint32_t at[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      key[j] = ordered(z[j]);
+      at[j] = j;
+    }
+#pragma unroll
+    for (int phase = 0; phase < 8; ++phase)
+#pragma unroll
+      for (int j = phase & 1; j < 7; j += 2) {
+        const bool swap = key[j] < key[j + 1];
+        exchange(key[j], key[j + 1]);
+        const uint32_t x = at[j];
+        at[j] = swap ? at[j + 1] : x;
+        at[j + 1] = swap ? x : at[j + 1];
+      }
+    places = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) places |= at[j] << (4 * j);
+  }
+  __device__ __forceinline__ void up(bool taken) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j) key[j] = taken ? key[j + 1] : key[j];
+    key[7] = taken ? 0u : key[7];
+    places = taken ? places >> 4 : places;
+  }
+};
+
+// One round: the candidate that is chosen, in every lane of the group.
+// `key` 0: there is none, `expert` is -1.
+struct Choice {
+  uint32_t key;
+  int expert;
+};
+template <int LPT, int C>
+__device__ __forceinline__ Choice choose(Run<uint16_t> (&run)[C], int) {
+  uint32_t best = run[0].key[0];
+#pragma unroll
+  for (int c = 1; c < C; ++c) best = run[c].key[0] > best ? run[c].key[0] : best;
+  best = lanes_max_u32<LPT>(best);
+#pragma unroll
+  for (int c = 0; c < C; ++c) run[c].up(run[c].key[0] == best);
+  return {best, best ? int(0xFFFF - (best & 0xFFFFu)) : -1};
+}
+template <int LPT, int C>
+__device__ __forceinline__ Choice choose(Run<float> (&run)[C], int lane) {
+  uint32_t best = run[0].key[0];
+#pragma unroll
+  for (int c = 1; c < C; ++c) best = run[c].key[0] > best ? run[c].key[0] : best;
+  best = lanes_max_u32<LPT>(best);
+  uint32_t mine[C], first = 0xFFFFFFFFu;
+#pragma unroll
+  for (int c = C - 1; c >= 0; --c) {
+    mine[c] = uint32_t((c * LPT + lane) * 8) + (run[c].places & 7u);
+    first = run[c].key[0] == best ? mine[c] : first;
+  }
+  first = lanes_min_u32<LPT>(first);
+#pragma unroll
+  for (int c = 0; c < C; ++c) run[c].up(mine[c] == first);
+  return {best, best ? int(first) : -1};
+}
+
 // slope of one expert, for n > 0
 __device__ __forceinline__ float slope_of(int64_t E, int64_t k, int count, int tokens) {
   return tokens > 0 ? float(E) * float(count) / (float(k) * float(tokens) * float(tokens)) : 0.0f;
@@ -118,40 +231,26 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[c][j] = __builtin_fmaf(tok.x[c][j], tok.inv, acc[c][j]);
 
+    Run<T> run[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) run[c].sort(tok.z[c], (c * LPT + lane) * 8);
     float w[ROUNDS], total = 0.0f;
     int ex[ROUNDS];
 #pragma unroll
-    for (int r = 0; r < ROUNDS; ++r) {
-      w[r] = 0.0f;
+    for (int r = 0; r < ROUNDS; ++r) {             // lane j of the group keeps choice r LPT + j
+      uint32_t key = 0;
       ex[r] = -1;
       for (int j = r * LPT; j < k && j < (r + 1) * LPT; ++j) {
-        float best = __uint_as_float(kNegInf);
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) best = __builtin_fmaxf(best, tok.z[c][i]);
-        best = lanes_max<LPT>(best);
-        uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-        for (int c = C - 1; c >= 0; --c)
-#pragma unroll
-          for (int i = 7; i >= 0; --i)
-            at = tok.z[c][i] == best ? uint32_t((c * LPT + lane) * 8 + i) : at;
-        at = lanes_min_u32<LPT>(at);
-        const bool found = best > __uint_as_float(kNegInf);
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            tok.z[c][i] = at == uint32_t((c * LPT + lane) * 8 + i) ? __uint_as_float(kNegInf) : tok.z[c][i];
-        const float wj = found ? tok.term(best) * tok.inv : 0.0f;
-        total += wj;
+        const Choice best = choose<LPT, C>(run, lane);
         if (lane == j - r * LPT) {
-          w[r] = wj;
-          ex[r] = found ? int(at) : -1;
+          key = best.key;
+          ex[r] = best.expert;
         }
       }
+      w[r] = key ? tok.term(logit_of(key, T())) * tok.inv : 0.0f;
+      total += w[r];
     }
+    if (p.renormalize) total = lanes_sum<LPT>(total);
     const float scale = p.renormalize ? (total > 0.0f ? 1.0f / total : 0.0f) : 1.0f;
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {

@@ -18,28 +18,27 @@ __device__ __forceinline__ void keep(Row8<float>& x, int n) {
     x.b[i] = 4 + i < n ? x.b[i] : 0.0f;
   }
 }
-// kReadOnce: past the caches, for what nobody reads again.
-enum Reuse { kReadAgain, kReadOnce };
-template <Reuse U, typename V>
+// ONCE: past the caches, for what nobody reads again.
+template <bool ONCE, typename V>
 __device__ __forceinline__ V load_vec(const void* p) {
-  if constexpr (U == kReadOnce) return __builtin_nontemporal_load(static_cast<const V*>(p));
+  if constexpr (ONCE) return __builtin_nontemporal_load(static_cast<const V*>(p));
   else return *static_cast<const V*>(p);
 }
-template <Reuse U>
-__device__ __forceinline__ void load_chunks(Row8<uint16_t>& x, const uint16_t* p, int) { x.w = load_vec<U, u32x4>(p); }
-template <Reuse U>
+template <bool ONCE>
+__device__ __forceinline__ void load_chunks(Row8<uint16_t>& x, const uint16_t* p, int) { x.w = load_vec<ONCE, u32x4>(p); }
+template <bool ONCE>
 __device__ __forceinline__ void load_chunks(Row8<float>& x, const float* p, int n) {
-  x.a = load_vec<U, v4f>(p);
-  if (n > 4) x.b = load_vec<U, v4f>(p + 4);
+  x.a = load_vec<ONCE, v4f>(p);
+  if (n > 4) x.b = load_vec<ONCE, v4f>(p + 4);
 }
 
 // Elements [col, col + 8) of a row of `cols`; zeros beyond its end.  Rows are
 // 16-byte aligned, and the 16 bytes that an element lies in are read whole:
 // they are in one page, and what the row does not own of them is not used.
-template <Reuse U = kReadAgain, typename T>
+template <bool ONCE = false, typename T>
 __device__ __forceinline__ void load_raw(Row8<T>& x, const T* row, int col, int cols) {
   x.zero();
-  if (col < cols) load_chunks<U>(x, row + col, cols - col);
+  if (col < cols) load_chunks<ONCE>(x, row + col, cols - col);
   if (col + 8 > cols && col < cols) keep(x, cols - col);
 }
 
