@@ -93,7 +93,7 @@ hipError_t launch_moe_route_backward(const RouteBwdArgs& p, bool bf16, hipStream
 inline int64_t route_lanes(int64_t E) { return E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ? 32 : 64; }
 inline int64_t route_parts(int64_t T, int64_t E) {
   const int64_t few = 2 * 256 / route_lanes(E), turns = (T * route_lanes(E) + 1023) / 1024;
-  return T <= few ? 1 : turns < 2 ? 2 : turns < 512 ? turns : 512;
+  return T <= few ? 1 : turns < 2 ? 2 : turns < 256 ? turns : 256;
 }
 // Sums of p, counts, tokens, and the loss's shares of up to 16 workgroups.
 inline int64_t route_workspace(int64_t T, int64_t E) {

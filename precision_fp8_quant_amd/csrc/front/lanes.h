@@ -49,6 +49,21 @@ template <int N> __device__ __forceinline__ uint32_t lanes_min_u32(uint32_t v) {
   return lanes_reduce<N>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }
 
+// v summed over the lanes that have the same place in their group of N, in each of them.
+template <int N>
+__device__ __forceinline__ float groups_sum(float v) {
+  if constexpr (N <= 8) v += __uint_as_float(dpp<0x128>(__float_as_uint(v)));        // row_ror by 8: the other half row
+  if constexpr (N <= 16) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(uint32_t(a[0])) + __uint_as_float(uint32_t(a[1]));
+  }
+  if constexpr (N <= 32) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(uint32_t(a[0])) + __uint_as_float(uint32_t(a[1]));
+  }
+  return v;
+}
+
 // Sum over the TPR threads that share a row: a group of lanes, a wave, or the
 // whole workgroup through `part`, one word per wave.  With TPR > 64 every
 // thread of the workgroup calls it; `part` may be written again after the next

