@@ -15,8 +15,10 @@
  * launched, row-major matrices with leading dimensions in elements, 16-byte
  * aligned pointers and leading dimensions of a multiple of 16 bytes, finite
  * inputs (but for the logits of moe_route, see there), outputs that overlap
- * neither inputs nor each other.  Bytes of a row beyond its columns are
- * neither read nor written, unless stated.
+ * neither inputs nor each other.  Rows of inputs are read in whole 16-byte
+ * chunks: the bytes from their last column up to the next multiple of 16 may be
+ * read, and their values do not matter.  Bytes of an output's row beyond its
+ * columns are left as they are.
  *
  * A workspace is scratch memory of the caller's, 16-byte aligned, of the bytes
  * that the operator's own *_workspace function says (0: none, may be NULL;
@@ -160,9 +162,9 @@ int64_t fp8q_moe_route_workspace(int64_t T, int64_t E);
  * dloss    : optional (NULL: zero): FP32 [1] on the device, the gradient that
  *            reaches the loss (the loss's coefficient included).
  * dlogits  : dZ[T][E], leading dimension ld_dz, z_dtype, rounded once from FP32.
- *            Zeros for tokens that do not count (experts[t][0] == -1), whose
+ *            Zeros for tokens that do not count (experts[t][0] < 0), whose
  *            logits and dweights are not used.
- * Experts outside [0, E) contribute nothing.  Sizes as in moe_route; T == 0 is
+ * Other experts outside [0, E) contribute nothing.  Sizes as in moe_route; T == 0 is
  * a no-op.
  */
 int moe_route_backward(const void* logits, int64_t ld_z, int z_dtype, int64_t T, int64_t E, int64_t k,

@@ -101,17 +101,24 @@ __device__ __forceinline__ int block_exclusive(int v, int* wave_sum, int* total)
 // The tile map and the rows that hold no token, by 1024 threads: thread e < E
 // has expert e's count and first tile.
 __device__ __forceinline__ void write_maps(const DispatchArgs& p, int count, int first, int tiles_used, int (*place)[2]) {
-  const int t = threadIdx.x, tiles = int(p.M_total >> 7);
-  const int mine = (count + 127) >> 7;
-  if (t < int(p.E)) {
-    for (int i = 0; i < mine; ++i) p.group_of_mtile[first + i] = t;
+  const int t = threadIdx.x, tiles = int(p.M_total >> 7), E = int(p.E);
+  if (t < E) {
     place[t][0] = first * 128 + count;             // padding rows: [0] to [1]
-    place[t][1] = (first + mine) * 128;
+    place[t][1] = (first + ((count + 127) >> 7)) * 128;
   }
   for (int i = tiles_used + t; i < tiles; i += 1024) p.group_of_mtile[i] = -1;
   for (int64_t i = int64_t(tiles_used) * 128 + t; i < p.M_total; i += 1024) p.token_of_row[i] = -1;
   __syncthreads();
-  for (int i = t; i < int(p.E) * 128; i += 1024) {
+  for (int i = t; i < tiles_used; i += 1024) {     // the first expert that ends behind the tile's first row
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (place[mid][1] > i * 128) hi = mid;
+      else lo = mid + 1;
+    }
+    p.group_of_mtile[i] = lo;
+  }
+  for (int i = t; i < E * 128; i += 1024) {
     const int row = place[i >> 7][0] + (i & 127);
     if (row < place[i >> 7][1]) p.token_of_row[row] = -1;
   }

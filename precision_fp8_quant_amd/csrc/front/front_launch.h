@@ -57,8 +57,8 @@ constexpr int64_t kMaxNormD = 32768;
 // column.  Beyond 256 of them a workgroup takes two rows before there are more:
 // the second kernel reads every part.
 inline int64_t norm_bwd_parts(int64_t M, int64_t D) {
-  const int64_t rows = D <= 1024 ? 4 : 1, want = (M + rows - 1) / rows, most = D <= 4096 ? 512 : 256;
-  const int64_t parts = want <= 256 ? want : (want + 1) / 2 > 256 ? (want + 1) / 2 : 256;
+  const int64_t rows = D <= 1024 ? 4 : 1, want = M / rows + (M % rows != 0), most = D <= 4096 ? 512 : 256;
+  const int64_t half = want / 2 + want % 2, parts = want <= 256 ? want : half > 256 ? half : 256;
   return parts < most ? parts : most;
 }
 inline int64_t norm_bwd_workspace(int64_t M, int64_t D) { return norm_bwd_parts(M, D) * ((D + 7) / 8 * 8) * 4; }

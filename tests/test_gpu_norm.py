@@ -315,3 +315,51 @@ def test_norm_refusals():
     with pytest.raises(fp8q.Fp8qError) as e:
         fp8q.rmsnorm_backward(x, x, w, f(4), dx=x)
     assert e.value.status == fp8q.ERR_ALIAS
+
+
+# ---------------------------------------------------------------------------
+# Inputs of more than 96 MB are read past the caches, by kernels of their own
+# ---------------------------------------------------------------------------
+BIG = 96 << 20
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [512, 1024, 2048, 4096, 7168, 16384, 32768])
+def test_norms_of_many_rows_agree_with_those_of_few(d, dtype):
+    """Every width's kernels, in all forms: the last rows are what a call on them alone gives."""
+    fp8q = require_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    es = 2 if dtype == BF else 4
+    m = BIG // es // d + 130
+    lo = (m - 70) // 128 * 128
+    x = torch.randn((m, d), generator=gen, device="cuda", dtype=dtype)
+    r = torch.randn((m, d), generator=gen, device="cuda", dtype=dtype)
+    w = (1.0 + 0.2 * torch.randn(d, generator=gen, device="cuda")).to(dtype)
+    xs, rs = x[lo:].clone(), r[lo:].clone()
+
+    def rows(t):                                          # the tail of an output, whichever way it lies
+        return t[lo:] if t.shape[0] == m else t[:, lo:]
+
+    for res in (None, r):
+        small = None if res is None else rs
+        for call in (lambda a, b: fp8q.fp8_rmsnorm(a, w, residual=b, save_rstd=True, save_y=True),
+                     lambda a, b: fp8q.fp8_rmsnorm(a, w, residual=b, mode=fp8q.POW2),
+                     lambda a, b: fp8q.int8_rmsnorm(a, w, residual=b)):
+            for got, want in zip(call(x, res), call(xs, small)):
+                assert torch.equal(rows(got), want)
+        got, want = fp8q.fp8_rmsnorm(x, w, residual=res, transposed=True), fp8q.fp8_rmsnorm(xs, w, residual=small, transposed=True)
+        assert torch.equal(got[0][lo:], want[0]) and torch.equal(got[1][:, lo:], want[1])
+        assert torch.equal(got[2][:, lo:], want[2]) and torch.equal(got[3][lo // 128:], want[3])
+    rstd = fp8q.int8_rmsnorm(x, w, save_rstd=True)[2]
+    for dh in (None, r):
+        dx, dw = fp8q.rmsnorm_backward(r, x, w, rstd, dh=dh)
+        dx1, _ = fp8q.rmsnorm_backward(rs, xs, w, rstd[lo:].clone(), dh=None if dh is None else rs)
+        assert torch.equal(dx[lo:], dx1)
+        ref = torch.zeros(d, dtype=torch.float64, device="cuda")
+        size = torch.zeros_like(ref)
+        for i in range(0, m, 8192):
+            z = r[i:i + 8192].double() * x[i:i + 8192].double() * rstd[i:i + 8192].double()[:, None]
+            ref += z.sum(0)
+            size += z.abs().sum(0)
+        steps = m / 256 + 60                              # at least 256 rows at a time
+        assert bool(((dw.double() - ref).abs() <= steps * U * size).all())
