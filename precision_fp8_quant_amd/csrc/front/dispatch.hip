@@ -178,15 +178,15 @@ __global__ __launch_bounds__(1024) void plan_count_kernel(DispatchArgs p, int64_
 
 // Up to 16 threads (1024 over E rounded up to a power of two) sum an expert's
 // counts over consecutive pieces of the workgroups: all of them for the first
-// rows of the experts, those before this one for its own.  The first workgroup
-// also writes the maps.
+// rows of the experts, those before this one for its own.  One workgroup more
+// than there are of chunks writes the maps.
 __global__ __launch_bounds__(1024) void plan_place_kernel(DispatchArgs p, int64_t chunk, int bits) {
   __shared__ int next[16][kMaxExperts];
   __shared__ int place[kMaxExperts][2];
   __shared__ int wave_sum[16];
   int* sums = next[0];                             // [2][1024], before next[] is filled
   const int t = threadIdx.x, wave = t >> 6, E = int(p.E), ep = 1 << bits, share = bits < 6 ? 16 : 1024 >> bits;
-  const int blocks = gridDim.x, mine = blockIdx.x;
+  const int blocks = int(gridDim.x) - 1, mine = blockIdx.x;
   const int64_t c = int64_t(mine) * 16 + wave, slots = p.T * p.k, begin = c * chunk;
   const int64_t end = begin + chunk < slots ? begin + chunk : slots;
   const int* group_counts = p.hist + int64_t(blocks) * 16 * E;
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(1024) void plan_place_kernel(DispatchArgs p, int64_
     }
   }
   int own[16];
-  if (t < E) {
+  if (t < E && mine < blocks) {
 #pragma unroll
     for (int w = 0; w < 16; ++w) own[w] = p.hist[(int64_t(mine) * 16 + w) * E + t];
   }
@@ -219,6 +219,10 @@ __global__ __launch_bounds__(1024) void plan_place_kernel(DispatchArgs p, int64_
     }
   int used;
   const int first = block_exclusive((all + 127) >> 7, wave_sum, &used);   // its barrier: sums[] has been read
+  if (mine == blocks) {                            // uniform over the workgroup
+    write_maps(p, all, first, used, place);
+    return;
+  }
   if (t < E) {
     int row = first * 128 + before;
 #pragma unroll
@@ -227,7 +231,6 @@ __global__ __launch_bounds__(1024) void plan_place_kernel(DispatchArgs p, int64_
       row += own[w];
     }
   }
-  if (blockIdx.x == 0) write_maps(p, all, first, used, place);
   __syncthreads();
   place_chunk(p, begin, end, bits, next[wave], experts);
 }
@@ -286,7 +289,7 @@ hipError_t launch_moe_dispatch(const DispatchArgs& p, hipStream_t st) {
     hipLaunchKernelGGL(plan_count_kernel, dim3(groups), dim3(1024), 0, st, p, chunk);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(plan_place_kernel, dim3(groups), dim3(1024), 0, st, p, chunk, bits);
+    hipLaunchKernelGGL(plan_place_kernel, dim3(groups + 1), dim3(1024), 0, st, p, chunk, bits);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.T == 0 || p.D == 0) return e;

@@ -53,11 +53,11 @@ hipError_t launch_rmsnorm_backward(const NormBwdArgs& p, bool x_bf16, bool w_bf1
 constexpr int64_t kMaxNormD = 32768;
 
 // Rows that a workgroup of the gradient kernel has in hand (a wave each up to
-// 1024 channels), and workgroups, each of which leaves one partial sum of dw per
+// 1024 channels, 16 lanes up to 128), and workgroups, each of which leaves one partial sum of dw per
 // column.  Beyond 256 of them a workgroup takes two rows before there are more:
 // the second kernel reads every part.
 inline int64_t norm_bwd_parts(int64_t M, int64_t D) {
-  const int64_t rows = D <= 1024 ? 4 : 1, want = M / rows + (M % rows != 0), most = D <= 4096 ? 512 : 256;
+  const int64_t rows = D <= 128 ? 16 : D <= 1024 ? 4 : 1, want = M / rows + (M % rows != 0), most = D <= 4096 ? 512 : 256;
   const int64_t half = want / 2 + want % 2, parts = want <= 256 ? want : half > 256 ? half : 256;
   return parts < most ? parts : most;
 }
@@ -88,12 +88,16 @@ struct RouteBwdArgs {
 };
 hipError_t launch_moe_route_backward(const RouteBwdArgs& p, bool bf16, hipStream_t st);
 
-// Workgroups of the forward kernel.  Up to 64 tokens (of 64 experts; 8 of 1024)
-// one of 256 threads does it all; otherwise they have 1024 threads.
+// Lanes of a token.
 inline int64_t route_lanes(int64_t E) { return E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ? 32 : 64; }
+// Up to so many tokens (64 of 64 experts, 8 of 1024) one workgroup of 256 threads does it all.
+inline int64_t route_few(int64_t E) { return 2 * 256 / route_lanes(E); }
+// Workgroups of the forward kernel, of 1024 threads beyond that.  One alone also
+// finishes the sums, in up to three turns (384 tokens of 64 experts); more need
+// a second kernel.
 inline int64_t route_parts(int64_t T, int64_t E) {
-  const int64_t few = 2 * 256 / route_lanes(E), turns = (T * route_lanes(E) + 1023) / 1024;
-  return T <= few ? 1 : turns < 2 ? 2 : turns < 256 ? turns : 256;
+  const int64_t turns = (T * route_lanes(E) + 1023) / 1024;
+  return turns <= 3 ? 1 : turns < 256 ? turns : 256;
 }
 // Sums of p, counts, tokens, and the loss's shares of up to 16 workgroups.
 inline int64_t route_workspace(int64_t T, int64_t E) {

@@ -63,12 +63,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(NormArgs
     float v[R][8], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
+      const int col = (i * TPR + t) * 8;
+      trim(xr[i], col, D);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] = xr[i].get(j);
       if (r) {
+        trim(rr[i], col, D);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] += rr[i].get(j);
-        store_raw(h + row * p.ld_h, (i * TPR + t) * 8, D, v[i]);
+        store_raw(h + row * p.ld_h, col, D, v[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = held(v[i][j], T());
       }
@@ -82,16 +85,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(NormArgs
       float row_a = 0.0f;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
+        const int col = (i * TPR + t) * 8;
+        trim(wr[i], col, D);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * wr[i].get(j);
-        if (y) store_raw(y + row * p.ld_y, (i * TPR + t) * 8, D, v[i]);
+        if (y) store_raw(y + row * p.ld_y, col, D, v[i]);
         const float a = max_abs8(v[i]);
         if constexpr (OUT == kOutInt8) {
           row_a = __builtin_fmaxf(row_a, a);
         } else {
           constexpr int MODE = OUT == kOutFp8Pow2 ? kModePow2 : kModeMaxAbs;
           const ScalePair sp = scale_from_amax_bits<MODE>(row16_max_u32(__float_as_uint(a)));
-          const int col = (i * TPR + t) * 8;
           if (col < D) {
             *reinterpret_cast<uint2*>(p.q + row * p.ld_q + col) =
                 uint2{quant4(v[i][0], v[i][1], v[i][2], v[i][3], sp.inv), quant4(v[i][4], v[i][5], v[i][6], v[i][7], sp.inv)};
@@ -214,6 +218,7 @@ hipError_t launch_rows(const NormArgs& p, hipStream_t st) {
 
 template <typename T, typename W, int OUT>
 hipError_t launch_out(const NormArgs& p, hipStream_t st) {
+  if (p.D <= 128) return launch_rows<T, W, 16, 1, OUT>(p, st);
   if (p.D <= 512) return launch_rows<T, W, 64, 1, OUT>(p, st);
   if (p.D <= 1024) return launch_rows<T, W, 64, 2, OUT>(p, st);
   if (p.D <= 2048) return launch_rows<T, W, 256, 1, OUT>(p, st);

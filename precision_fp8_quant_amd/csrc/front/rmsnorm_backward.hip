@@ -54,7 +54,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if constexpr (LATE) load_raw(wr[i], weight, (i * TPR + t) * 8, D);
+      const int col = (i * TPR + t) * 8;
+      if constexpr (LATE) load_raw(wr[i], weight, col, D);
+      trim(yr[i], col, D);
+      trim(hr[i], col, D);
+      trim(wr[i], col, int(p.D));
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float z = yr[i].get(j) * (hr[i].get(j) * rs);
@@ -138,7 +142,8 @@ template <typename T, typename W>
 hipError_t launch(const NormBwdArgs& p, hipStream_t st) {
   const int64_t parts = norm_bwd_parts(p.M, p.D);  // norm_bwd_threads() says TPR
   if (parts > 0) {
-    if (p.D <= 512) launch_rows<T, W, 64, 1>(p, parts, st);
+    if (p.D <= 128) launch_rows<T, W, 16, 1>(p, parts, st);
+    else if (p.D <= 512) launch_rows<T, W, 64, 1>(p, parts, st);
     else if (p.D <= 1024) launch_rows<T, W, 64, 2>(p, parts, st);
     else if (p.D <= 2048) launch_rows<T, W, 256, 1>(p, parts, st);
     else if (p.D <= 4096) launch_rows<T, W, 512, 1>(p, parts, st);

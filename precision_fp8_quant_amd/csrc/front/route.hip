@@ -41,7 +41,7 @@ struct Token {
     for (int c = 0; c < C; ++c) {
       const int e0 = (c * LPT + lane) * 8;
       Row8<T> raw;
-      load_raw(raw, row, e0, cols);
+      load_raw(raw, row, e0, cols);                // not trimmed: z[] is
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         z[c][j] = e0 + j < cols ? raw.get(j) : ninf;
@@ -342,6 +342,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
   for (int c = 0; c < C; ++c) {
     Row8<float> s;
     load_raw(s, p.slope, (c * LPT + lane) * 8, p.dloss ? E : 0);
+    trim(s, (c * LPT + lane) * 8, E);
 #pragma unroll
     for (int j = 0; j < 8; ++j) every[c][j] = s.get(j) * dloss;
   }
@@ -428,7 +429,7 @@ template <typename T>
 hipError_t launch_route_t(const RouteArgs& p, hipStream_t st) {
   const int64_t parts = route_parts(p.T, p.E);
   const hipError_t e = by_experts(p.E, [&](auto lpt, auto c) {
-    if (parts == 1) hipLaunchKernelGGL((route_kernel<T, lpt(), c(), 256>), dim3(1), dim3(256), 0, st, p);
+    if (p.T <= route_few(p.E)) hipLaunchKernelGGL((route_kernel<T, lpt(), c(), 256>), dim3(1), dim3(256), 0, st, p);
     else hipLaunchKernelGGL((route_kernel<T, lpt(), c(), 1024>), dim3(unsigned(parts)), dim3(1024), 0, st, p);
     return hipGetLastError();
   });

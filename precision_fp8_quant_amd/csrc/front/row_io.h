@@ -32,13 +32,17 @@ __device__ __forceinline__ void load_chunks(Row8<float>& x, const float* p, int 
   if (n > 4) x.b = load_vec<ONCE, v4f>(p + 4);
 }
 
-// Elements [col, col + 8) of a row of `cols`; zeros beyond its end.  Rows are
-// 16-byte aligned, and the 16 bytes that an element lies in are read whole:
-// they are in one page, and what the row does not own of them is not used.
+// Elements [col, col + 8) of a row of `cols`, in two steps.  load_raw: rows are
+// 16-byte aligned, and the 16 bytes that an element lies in are read whole; they
+// are in one page.  trim: zeros for what the row does not own of them.  (One
+// step would have the threads at a row's end wait for each of their loads.)
 template <bool ONCE = false, typename T>
 __device__ __forceinline__ void load_raw(Row8<T>& x, const T* row, int col, int cols) {
   x.zero();
   if (col < cols) load_chunks<ONCE>(x, row + col, cols - col);
+}
+template <typename T>
+__device__ __forceinline__ void trim(Row8<T>& x, int col, int cols) {
   if (col + 8 > cols && col < cols) keep(x, cols - col);
 }
 
