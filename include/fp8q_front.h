@@ -132,7 +132,7 @@ int64_t fp8q_rmsnorm_backward_workspace(int64_t M, int64_t D);
  *            chosen.  A token with fewer than k others gets them alone, and
  *            expert -1 with weight 0 in the remaining places.
  * valid    : optional (NULL: all): uint8 [T]; 0 for a token that does not
- *            count, whose logits are not read.  It, and a token whose logits
+ *            count, whose logits do not matter.  It, and a token whose logits
  *            are all minus infinity, has experts -1 and weights 0.
  * renormalize : 0 or 1.
  * weights  : FP32 [T][k], packed.   experts : int32 [T][k], packed.
@@ -163,7 +163,7 @@ int64_t fp8q_moe_route_workspace(int64_t T, int64_t E);
  *            reaches the loss (the loss's coefficient included).
  * dlogits  : dZ[T][E], leading dimension ld_dz, z_dtype, rounded once from FP32.
  *            Zeros for tokens that do not count (experts[t][0] < 0), whose
- *            logits and dweights are not used.
+ *            logits and dweights do not matter.
  * Other experts outside [0, E) contribute nothing.  Sizes as in moe_route; T == 0 is
  * a no-op.
  */

@@ -26,25 +26,33 @@ namespace {
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr uint32_t kNegInf = 0xFF800000u;
 
+// A lane's logits of one token as they lie in memory.
+template <typename T, int LPT, int C>
+struct Logits {
+  Row8<T> raw[C];
+  __device__ __forceinline__ void load(const T* row, int lane, int cols) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) load_raw(raw[c], row, (c * LPT + lane) * 8, cols);   // Token trims them
+  }
+};
+
 // Logits of one token, its softmax's terms and whether it counts.  cols: E, or
-// 0 for a token whose logits are not read.
+// 0 for a token that does not.
 template <typename T, int LPT, int C>
 struct Token {
   float z[C][8], x[C][8];         // logits (minus infinity beyond the row), exp(z - m)
   float m, inv;                   // the maximum (0 where all are minus infinity), 1 / sum of x (0 there)
   bool counts;
 
-  __device__ __forceinline__ void load(const T* row, int lane, int cols) {
+  __device__ __forceinline__ Token(const Logits<T, LPT, C>& from, int lane, int cols) {
     const float ninf = __uint_as_float(kNegInf);
     float top = ninf;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int e0 = (c * LPT + lane) * 8;
-      Row8<T> raw;
-      load_raw(raw, row, e0, cols);                // not trimmed: z[] is
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        z[c][j] = e0 + j < cols ? raw.get(j) : ninf;
+        z[c][j] = e0 + j < cols ? from.raw[c].get(j) : ninf;
         top = __builtin_fmaxf(top, z[c][j]);
       }
     }
@@ -207,9 +215,10 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
   for (int64_t t0 = int64_t(blockIdx.x) * G; t0 < p.T; t0 += int64_t(gridDim.x) * G) {
     const int64_t t = t0 + group;
     const bool here = t < p.T;
-    const bool read = here && (!p.valid || p.valid[t] != 0);
-    Token<T, LPT, C> tok;
-    tok.load(logits + t * p.ld_z, lane, read ? E : 0);
+    Logits<T, LPT, C> z;
+    z.load(logits + t * p.ld_z, lane, here ? E : 0);
+    const bool valid = here && (!p.valid || p.valid[t] != 0);
+    Token<T, LPT, C> tok(z, lane, valid ? E : 0);
     n += tok.counts;
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -349,9 +358,10 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
   for (int64_t t0 = int64_t(blockIdx.x) * G; t0 < p.T; t0 += int64_t(gridDim.x) * G) {
     const int64_t t = t0 + group;
     const bool here = t < p.T;
+    Logits<T, LPT, C> z;
+    z.load(logits + t * p.ld_z, lane, here ? E : 0);
     const bool counts = here && p.experts[t * k] >= 0;
-    Token<T, LPT, C> tok;
-    tok.load(logits + t * p.ld_z, lane, counts ? E : 0);
+    Token<T, LPT, C> tok(z, lane, counts ? E : 0);
     float dp[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c)
