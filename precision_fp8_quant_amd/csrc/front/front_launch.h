@@ -88,8 +88,8 @@ struct RouteBwdArgs {
 };
 hipError_t launch_moe_route_backward(const RouteBwdArgs& p, bool bf16, hipStream_t st);
 
-// Lanes of a token.
-inline int64_t route_lanes(int64_t E) { return E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ? 32 : 64; }
+// Lanes of a token in the forward kernel.
+inline int64_t route_lanes(int64_t E) { return E <= 128 ? 8 : E <= 256 ? 16 : E <= 512 ? 32 : 64; }
 // Up to so many tokens (64 of 64 experts, 8 of 1024) one workgroup of 256 threads does it all.
 inline int64_t route_few(int64_t E) { return 2 * 256 / route_lanes(E); }
 // Workgroups of the forward kernel, of 1024 threads beyond that.  One alone also
