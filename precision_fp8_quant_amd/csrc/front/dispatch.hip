@@ -6,14 +6,16 @@
 // does not depend on timing.  A wave takes a chunk of slots 64 at a time: lanes
 // of equal experts find each other by one ballot per bit of the expert, a
 // lane's place is the expert's running count plus its equals in lower lanes.
-//   up to 8192 slots   one workgroup: counts of its 16 waves' chunks, their
+//   up to 1024 slots   no plan of its own: every workgroup of the one kernel finds
+//                      the experts' tiles and its tile's tokens for itself
+//   up to 8192         one workgroup: counts of its 16 waves' chunks, their
 //                      prefix sums and the tile map, the rows
 //   beyond             two kernels of up to 128 workgroups of 16 chunks: the counts
 //                      of chunks and workgroups; then the rows, every workgroup
 //                      summing the others' counts for itself
-// Then one kernel moves codes and scales: a token's row is read once and
-// written to its k places; scales, which lie transposed, are written in runs of
-// a tile's 128 rows, with the padding rows of the tile.
+// Then (beyond 1024 slots) one kernel moves codes and scales: a token's row is
+// read once and written to its k places; scales, which lie transposed, are
+// written in runs of a tile's 128 rows, with the padding rows of the tile.
 #include "front_launch.h"
 #include "lanes.h"
 #include "row_io.h"
@@ -270,6 +272,122 @@ __global__ __launch_bounds__(256) void move_kernel(DispatchArgs p, int64_t tile_
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few slots, as in a decode batch, whose bytes are mostly padding: one launch,
+// work units of a tile's rows by 1024 codes.  Each workgroup counts all slots,
+// finds the expert of its tile and lists the tile's slots in their order; the
+// first piece of a tile also writes its part of the maps.
+// ---------------------------------------------------------------------------
+constexpr int kOneLaunch = int(kDispatchOneLaunch);
+
+__global__ __launch_bounds__(256) void dispatch_few_kernel(DispatchArgs p, int64_t pieces, int64_t units) {
+  constexpr int STEPS = kOneLaunch / 256;          // slots of a thread; a wave's are consecutive
+  constexpr int PER = int(kMaxExperts) / 256;      // experts of a thread
+  __shared__ int count[kMaxExperts];
+  __shared__ int token[128], slot_of[128];
+  __shared__ int wave_sum[4];
+  __shared__ int tile_expert, tile_skip;           // the tile's expert (-1: not in use), its slots in earlier tiles
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, E = int(p.E), slots = int(p.T * p.k), k = int(p.k);
+  const int slot0 = wave * (kOneLaunch / 4) + lane;
+  int e[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int s = slot0 + 64 * i;
+    e[i] = s < slots ? p.experts[s] : -1;
+  }
+  for (int x = t; x < int(kMaxExperts); x += 256) count[x] = 0;
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) e[i] = uint32_t(e[i]) < uint32_t(E) ? e[i] : -1;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i)
+    if (e[i] >= 0) atomicAdd(&count[e[i]], 1);     // integers: the order does not matter
+  __syncthreads();
+  // tiles before each of the thread's experts
+  int n[PER], mine = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    n[i] = (count[t * PER + i] + 127) >> 7;
+    mine += n[i];
+  }
+  int before = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(before, d, 64);
+    if (lane >= d) before += o;
+  }
+  if (lane == 63) wave_sum[wave] = before;
+  __syncthreads();
+  before -= mine;
+  for (int w = 0; w < wave; ++w) before += wave_sum[w];
+
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {      // block-uniform: barriers stay matched
+    const int tile = int(u / pieces), piece = int(u % pieces);
+    if (u == 0) {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i)
+        if (slot0 + 64 * i < slots && e[i] < 0) p.row_of_slot[slot0 + 64 * i] = -1;
+    }
+    if (t == 0) tile_expert = -1;
+    if (t < 128) token[t] = -1;
+    __syncthreads();
+    int first = before;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (tile >= first && tile < first + n[i]) {  // one thread's, for one expert
+        tile_expert = t * PER + i;
+        tile_skip = (tile - first) * 128;
+      }
+      first += n[i];
+    }
+    __syncthreads();
+    const int expert = tile_expert, skip = tile_skip;
+    // the expert's slots in the waves before this one, then one by one
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) at += __popcll(__ballot(expert >= 0 && e[i] == expert));
+    if (lane == 0) wave_sum[wave] = at;
+    __syncthreads();
+    at = -skip;
+    for (int w = 0; w < wave; ++w) at += wave_sum[w];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const bool hit = expert >= 0 && e[i] == expert;
+      const uint64_t all = __ballot(hit);
+      const int r = at + __popcll(all & ((uint64_t(1) << lane) - 1));
+      if (hit && r >= 0 && r < 128) {
+        token[r] = (slot0 + 64 * i) / k;
+        slot_of[r] = slot0 + 64 * i;
+      }
+      at += __popcll(all);
+    }
+    __syncthreads();
+    if (piece == 0) {
+      if (t == 0) p.group_of_mtile[tile] = expert;
+      if (t < 128) {
+        p.token_of_row[tile * 128 + t] = token[t];
+        if (token[t] >= 0) p.row_of_slot[slot_of[t]] = tile * 128 + t;
+      }
+    }
+    if (expert >= 0) {
+      const int64_t groups = p.D >> 7, g0 = int64_t(piece) * 8, g1 = g0 + 8 < groups ? g0 + 8 : groups;
+      const int row = t & 127, tok = token[row];
+      for (int64_t g = g0 + (t >> 7); g < g1; g += 2)
+        p.a_scales[g * p.M_total + tile * 128 + row] = tok >= 0 ? p.scales[g * p.T + tok] : __uint_as_float(kZeroScaleBits);
+      const int64_t col = int64_t(piece) * 1024 + lane * 16;
+      if (col < p.D) {
+#pragma unroll 8
+        for (int r = wave; r < 128; r += 4) {
+          u32x4 v = {0u, 0u, 0u, 0u};
+          if (token[r] >= 0) v = *reinterpret_cast<const u32x4*>(p.q + token[r] * p.ld_q + col);
+          *reinterpret_cast<u32x4*>(p.a + (int64_t(tile) * 128 + r) * p.ld_a + col) = v;
+        }
+      }
+    }
+    __syncthreads();                               // token[] and wave_sum[] are written again for the next unit
+  }
+}
+
 int bits_of(int64_t E) {                           // bits that tell E experts apart
   int b = 0;
   while ((int64_t(1) << b) < E) ++b;
@@ -280,6 +398,11 @@ int bits_of(int64_t E) {                           // bits that tell E experts a
 
 hipError_t launch_moe_dispatch(const DispatchArgs& p, hipStream_t st) {
   const int64_t slots = p.T * p.k;
+  if (slots <= kDispatchOneLaunch) {
+    const int64_t pieces = p.D > 1024 ? (p.D + 1023) / 1024 : 1, units = p.M_total / 128 * pieces;
+    hipLaunchKernelGGL(dispatch_few_kernel, dim3(grid_of(units, 256)), dim3(256), 0, st, p, pieces, units);
+    return hipGetLastError();
+  }
   const unsigned groups = unsigned(dispatch_groups(slots));
   const int bits = bits_of(p.E);
   if (groups == 0) {
