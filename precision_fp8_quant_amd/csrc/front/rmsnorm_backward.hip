@@ -7,6 +7,10 @@
 // 8 (i TPR + t)), and each thread keeps the sums of dw of its own columns over
 // all rows of its workgroup.  The workgroups' sums (in the workspace, one row
 // each) are added by a second kernel, in a fixed order: no atomics.
+// Bound by memory: 8192x7168 BF16 with dh 85 us, 5.5 TB/s (a large copy: 5.1), and 5
+// us for the sums.  The registers of the sums decide the shape: 1024 threads of one
+// run 91 us, 512 of two 93, 256 of four (one wave per SIMD) 107 with 256 workgroups
+// and the sums' kernel; 512 workgroups 93, 2048, with 59 MB of sums, 109.
 #include "front_launch.h"
 #include "lanes.h"
 #include "row_io.h"
@@ -143,6 +147,7 @@ hipError_t launch(const NormBwdArgs& p, hipStream_t st) {
   const int64_t parts = norm_bwd_parts(p.M, p.D);  // norm_bwd_threads() says TPR
   if (parts > 0) {
     if (p.D <= 128) launch_rows<T, W, 16, 1>(p, parts, st);
+    else if (p.D <= 256) launch_rows<T, W, 16, 2>(p, parts, st);
     else if (p.D <= 512) launch_rows<T, W, 64, 1>(p, parts, st);
     else if (p.D <= 1024) launch_rows<T, W, 64, 2>(p, parts, st);
     else if (p.D <= 2048) launch_rows<T, W, 256, 1>(p, parts, st);

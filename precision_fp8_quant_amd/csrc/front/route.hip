@@ -14,6 +14,10 @@
 // their p in registers, a wave its groups', a workgroup its waves'; workgroups
 // leave one row of sums and counts each, which a second kernel adds in a fixed
 // order.  With one workgroup it is all one launch.
+// Bound by instructions, more than half of them the choice: 65536 tokens, 8 of 64
+// experts BF16 11.3 us (6.0 without the choice; 16.6 with k scans of all logits
+// instead of sorted runs) and 3.4 for the sums, 8 of 256 FP32 34 us (14).  The gradient
+// is bound by memory: 8 of 256 FP32 30.6 us, 4.5 TB/s.
 #include "front_launch.h"
 #include "lanes.h"
 #include "row_io.h"

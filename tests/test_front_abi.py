@@ -115,7 +115,7 @@ def test_rmsnorm_backward_validation(want, kw):
 
 
 def _route(**kw):
-    v = dict(z=X, ldz=64, dt=fp8q.F32, t=300, e=60, k=8, valid=R, renorm=0, w=W, ex=H, c=S, loss=Y, slope=Q, ws=WS)
+    v = dict(z=X, ldz=64, dt=fp8q.F32, t=500, e=60, k=8, valid=R, renorm=0, w=W, ex=H, c=S, loss=Y, slope=Q, ws=WS)
     v.update(kw)
     return fp8q.lib.moe_route(v["z"], v["ldz"], v["dt"], v["t"], v["e"], v["k"], v["valid"], v["renorm"], v["w"], v["ex"],
                               v["c"], v["loss"], v["slope"], v["ws"], None)
