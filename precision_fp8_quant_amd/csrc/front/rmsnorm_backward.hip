@@ -22,8 +22,10 @@ namespace {
 template <typename T, typename W, int TPR, int R, bool ONCE>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel(NormBwdArgs p) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
-  // With four runs the registers hold no more than dy, h and the sums of dw.
+  // With four runs the registers hold no more than dy and h: the sums of dw are in LDS, each thread's its own
+  // (2048x32768 with dh, us: BF16 117, in registers, which spill, 194; FP32, which spills still, 390 and 566).
   constexpr bool LATE = R > 2;
+  __shared__ v4f far[LATE ? 2 * R : 1][LATE ? TPR : 1];
   __shared__ float part[2][NT / 64];
   const int t = threadIdx.x & (TPR - 1);
   const T* __restrict__ dy = static_cast<const T*>(p.dy);
@@ -33,12 +35,16 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
   const W* __restrict__ weight = static_cast<const W*>(p.weight);
   const float inv_d = 1.0f / float(p.D);
   Row8<W> wr[R];
-  float acc[R][8];
+  float acc[LATE ? 1 : R][8];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    if constexpr (!LATE) load_raw(wr[i], weight, (i * TPR + t) * 8, int(p.D));
+    if constexpr (LATE) {
+      far[2 * i][t] = far[2 * i + 1][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    } else {
+      load_raw(wr[i], weight, (i * TPR + t) * 8, int(p.D));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+      for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+    }
   }
   int odd = 0;
   // the last rows' threads stay for the barriers (TPR > 64) and lane exchanges of the others
@@ -63,11 +69,16 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
       trim(yr[i], col, D);
       trim(hr[i], col, D);
       trim(wr[i], col, int(p.D));
+      float z[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float z = yr[i].get(j) * (hr[i].get(j) * rs);
-        acc[i][j] += z;
-        sum = __builtin_fmaf(z, wr[i].get(j), sum);
+        z[j] = yr[i].get(j) * (hr[i].get(j) * rs);
+        if constexpr (!LATE) acc[i][j] += z[j];
+        sum = __builtin_fmaf(z[j], wr[i].get(j), sum);
+      }
+      if constexpr (LATE) {
+        far[2 * i][t] += v4f{z[0], z[1], z[2], z[3]};
+        far[2 * i + 1][t] += v4f{z[4], z[5], z[6], z[7]};
       }
       if constexpr (LATE) asm volatile("" ::: "memory");
     }
@@ -106,6 +117,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
       for (int k = 1; k < RPB; ++k) s += sums[k][c];
       out[c] = s;
     }
+  } else if constexpr (LATE) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if ((i * TPR + t) * 8 < dp) {
+        reinterpret_cast<v4f*>(out)[(i * TPR + t) * 2] = far[2 * i][t];
+        reinterpret_cast<v4f*>(out)[(i * TPR + t) * 2 + 1] = far[2 * i + 1][t];
+      }
   } else {
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -144,7 +162,7 @@ void launch_rows(const NormBwdArgs& p, int64_t parts, hipStream_t st) {
 
 template <typename T, typename W>
 hipError_t launch(const NormBwdArgs& p, hipStream_t st) {
-  const int64_t parts = norm_bwd_parts(p.M, p.D);  // norm_bwd_threads() says TPR
+  const int64_t parts = norm_bwd_parts(p.M, p.D);  // which counts on the rows of a workgroup here
   if (parts > 0) {
     if (p.D <= 128) launch_rows<T, W, 16, 1>(p, parts, st);
     else if (p.D <= 256) launch_rows<T, W, 16, 2>(p, parts, st);
