@@ -63,8 +63,8 @@ extern "C" {
  *            q_t[D][Mp], leading dimension ld_qt (bytes), and their scales
  *            [Mp/128][D], packed: the operand of fp8_gemm_blockscaled WGRAD.
  * Requires D a multiple of 128, at most 32768 (FP8Q_ERR_UNSUPPORTED).  The sum
- * of squares of a row of h must be finite in FP32.  M == 0 or D == 0 is a
- * no-op.
+ * of squares of a row of h, and y, must be finite in FP32.  M == 0 or D == 0 is
+ * a no-op.
  */
 int fp8_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_r, int x_dtype,
                 int64_t M, int64_t D,

@@ -59,7 +59,7 @@ bool read_once(int64_t M, int64_t D, int64_t es, int64_t n) {
 bool eps_ok(float eps) { return eps > 0.0f && eps <= 3.4028234664e38f; }   // false for NaN
 
 bool route_sizes_ok(int64_t T, int64_t E, int64_t k, int64_t most) {
-  return E >= 1 && E <= fp8q::kMaxExperts && k >= 1 && k <= fp8q::kMaxChosen && T < most / k;
+  return E >= 1 && E <= fp8q::kMaxExperts && k >= 1 && k <= fp8q::kMaxChosen && T <= (most - 1) / k;
 }
 
 }  // namespace

@@ -189,6 +189,8 @@ def test_sizes():
     assert lib.fp8q_rmsnorm_backward_workspace(0, 8) == 0 and lib.fp8q_rmsnorm_backward_workspace(MAX, 32768) > 0
     assert lib.fp8q_moe_route_workspace(1 << 31, 8) == -1 and lib.fp8q_moe_route_workspace(0, 8) == 0
     assert lib.fp8q_moe_dispatch_workspace(1 << 30, 1, 8) == -1
+    most = ((1 << 30) - 1) // 7                                # the last number of tokens whose slots are under 2^30
+    assert lib.fp8q_moe_max_rows(most, 7, 8) >= 7 * most and lib.fp8q_moe_max_rows(most + 1, 7, 8) == -1
     with pytest.raises(ValueError, match="no such sizes"):
         fp8q.moe_max_rows(5, 0, 8)
     # every row that any choice of experts fills fits: all slots in as many experts as there are, one row over each tile

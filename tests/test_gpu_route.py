@@ -64,7 +64,8 @@ def _check_route(out, z, k, valid, renormalize):
 
 
 SIZES = [(1, 1, 1), (1, 64, 8), (16, 64, 8), (3, 7, 7), (64, 64, 2), (65, 63, 9), (200, 65, 6), (300, 128, 32), (33, 129, 3),
-         (500, 200, 8), (50, 256, 1), (70, 257, 12), (130, 512, 8), (40, 513, 5), (20, 1000, 32), (9, 1024, 32), (1100, 8, 2)]
+         (500, 200, 8), (50, 256, 1), (70, 257, 12), (130, 512, 8), (40, 513, 5), (20, 1000, 32), (9, 1024, 32), (1100, 8, 2),
+         (700, 100, 8), (300, 1000, 8), (257, 1024, 31), (600, 300, 4)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
@@ -108,6 +109,7 @@ def test_moe_route_ties_and_zeros():
     z[1, ::2] = -0.0
     z[2, [70, 3, 41]] = 1.0
     z[3] = -5.0
+    z[3, [9, 50, 51]] = [1e-40, 3e-40, -1e-40]            # the smallest numbers are in order, too
     _check_route(fp8q.moe_route(dev(z), 6), z.astype(np.float64), 6, None, False)
 
 
@@ -266,6 +268,30 @@ def test_dispatch_at_tile_edges(counts):
     experts = np.concatenate([np.full(c, e, np.int32) for e, c in enumerate(counts)])
     experts = np.random.default_rng(1).permutation(experts)[:, None].copy()
     _check_dispatch(fp8q, experts, len(counts), 256, seed=6)
+
+
+@pytest.mark.parametrize("t", [40, 300, 9000])
+def test_dispatch_into_outputs_of_the_callers(t):
+    """Any of them given alone says how many rows there are; FP8 tensors are codes as bytes are."""
+    fp8q = require_gpu()
+    rng = np.random.default_rng(t)
+    ex = dev(rng.integers(-1, 9, (t, 4)).astype(np.int32))
+    q, s = fp8q.fp8_rmsnorm(torch.randn((t, 256), device="cuda"), torch.ones(256, device="cuda"))
+    rows = fp8q.moe_max_rows(t, 4, 9) + 256
+    i = lambda *sh: torch.full(sh, 99, dtype=torch.int32, device="cuda")       # noqa: E731
+    want = orf.dispatch(host(ex), 9, rows)
+    live = torch.from_numpy(want[2] >= 0).cuda()
+    of = dev(want[2]).long()[live]
+    for kw in (dict(a=torch.zeros((rows, 256), device="cuda").to(torch.float8_e4m3fn)),
+               dict(a_scales=torch.zeros((2, rows), device="cuda")), dict(group_of_mtile=i(rows // 128)),
+               dict(token_of_row=i(rows)), dict(token_of_row=i(rows), row_of_slot=i(t, 4))):
+        got = fp8q.fp8_moe_dispatch(ex, q.view(torch.float8_e4m3fn), s, 9, **kw)
+        for name, t_ in kw.items():
+            at = ("a", "a_scales", "group_of_mtile", "row_of_slot", "token_of_row").index(name)
+            assert got[at].data_ptr() == t_.data_ptr()
+        for g, w in zip(got[2:], want):
+            assert_bytes_equal(host(g), w, "maps")
+        assert torch.equal(got[0].view(torch.uint8)[live], q[of]) and torch.equal(got[1][:, live], s[:, of])
 
 
 def test_dispatch_empty():
