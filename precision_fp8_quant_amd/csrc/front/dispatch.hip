@@ -73,9 +73,9 @@ __device__ __forceinline__ void place_chunk(const DispatchArgs& p, int64_t begin
       const uint64_t below = same & below_mask;
       int row = -1;
       if (e[i] >= 0) row = next[e[i]] + __popcll(below);
-      asm volatile("" ::: "memory");               // the wave's reads come before its writes (LDS keeps their order)
+      wave_order();                                // the wave's reads come before its writes
       if (e[i] >= 0 && below == 0) next[e[i]] = row + __popcll(same);
-      asm volatile("" ::: "memory");
+      wave_order();
       if (slot < end) p.row_of_slot[slot] = row;
       if (e[i] >= 0) p.token_of_row[row] = int32_t(slot / p.k);
     }

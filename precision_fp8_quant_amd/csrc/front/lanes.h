@@ -8,6 +8,13 @@
 
 namespace fp8q {
 
+// What lanes of the wave wrote to LDS before it is there for those that read
+// behind it: LDS keeps a wave's order, the compiler has to.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  asm volatile("" ::: "memory");
+}
+
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return uint32_t(__builtin_amdgcn_mov_dpp(int(v), CTRL, 0xF, 0xF, true));

@@ -17,7 +17,7 @@
 // Bound by instructions, more than half of them the choice: 65536 tokens, 8 of 64
 // experts BF16 11.3 us (6.0 without the choice; 16.6 with k scans of all logits
 // instead of sorted runs) and 3.4 for the sums, 8 of 256 FP32 34 us (14).  The gradient
-// is bound by memory: 8 of 256 FP32 30.6 us, 4.5 TB/s.
+// is bound by memory: 8 of 256 FP32 30.0 us a call, 4.6 TB/s, 8 of 1000 (16384 tokens) 26.5, 5.0.
 #include "front_launch.h"
 #include "lanes.h"
 #include "row_io.h"
@@ -350,6 +350,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
   T* __restrict__ dlogits = static_cast<T*>(p.dlogits);
   const int E = int(p.E), k = int(p.k);
   const float dloss = p.dloss ? *p.dloss : 0.0f;
+  __shared__ __attribute__((aligned(16))) float rows[G][C * LPT * 8];
+  float* row = rows[group];                        // of the group's lanes alone, which are in one wave
   float every[C][8];                               // what reaches p of any token
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -364,28 +366,33 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
     const bool here = t < p.T;
     Logits<T, LPT, C> z;
     z.load(logits + t * p.ld_z, lane, here ? E : 0);
-    const bool counts = here && p.experts[t * k] >= 0;
+    int ex[ROUNDS];                                // lane j of the group has choice r LPT + j
+    float dc[ROUNDS];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+      const int j = r * LPT + lane;
+      ex[r] = here && j < k ? p.experts[t * k + j] : -1;
+      dc[r] = here && j < k && p.dweights ? p.dweights[t * k + j] : 0.0f;
+    }
+    const bool counts = __shfl(ex[0], 0, LPT) >= 0;
     Token<T, LPT, C> tok(z, lane, counts ? E : 0);
-    float dp[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dp[c][j] = every[c][j];
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<v4f*>(row + (c * LPT + lane) * 8 + 4 * q) =
+            v4f{every[c][4 * q], every[c][4 * q + 1], every[c][4 * q + 2], every[c][4 * q + 3]};
+    wave_order();
     if (p.dweights) {                              // uniform: all lanes exchange
-      int ex[ROUNDS];
-      float dc[ROUNDS], pe[ROUNDS], total = 0.0f, dot = 0.0f;
+      float pe[ROUNDS], total = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int r = 0; r < ROUNDS; ++r) {
-        const int j = r * LPT + lane;
-        ex[r] = -1;
-        dc[r] = pe[r] = 0.0f;
-        if (counts && j < k) {
-          const int e = p.experts[t * k + j];
-          if (e >= 0 && e < E) {
-            ex[r] = e;
-            dc[r] = p.dweights[t * k + j];
-            if (p.renormalize) pe[r] = tok.term(load1(logits + t * p.ld_z + e)) * tok.inv;
-          }
+        pe[r] = 0.0f;
+        if (counts && uint32_t(ex[r]) < uint32_t(E)) {
+          if (p.renormalize) pe[r] = tok.term(load1(logits + t * p.ld_z + ex[r])) * tok.inv;
+        } else {
+          ex[r] = -1;
+          dc[r] = 0.0f;
         }
         total += pe[r];
         dot = __builtin_fmaf(dc[r], pe[r], dot);
@@ -398,17 +405,24 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
 #pragma unroll
         for (int r = 0; r < ROUNDS; ++r) dc[r] = (dc[r] - mean) * inv;
       }
+      // To the experts' places by way of LDS, one after the other, so that an expert that comes more than once has one sum.
+      // (Compared with the index of every register in each of the k turns, 8 of 256: BF16 24.5 us, FP32 33.3; so 18.0, 30.0.)
 #pragma unroll
       for (int r = 0; r < ROUNDS; ++r)
-        for (int j = r * LPT; j < k && j < (r + 1) * LPT; ++j) {
-          const int e = __shfl(ex[r], j - r * LPT, LPT);
-          const float d = __shfl(dc[r], j - r * LPT, LPT);
-#pragma unroll
-          for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dp[c][i] += e == (c * LPT + lane) * 8 + i ? d : 0.0f;
-        }
+        for (int j = r * LPT; j < k && j < (r + 1) * LPT; ++j)
+          if (lane == j - r * LPT && ex[r] >= 0) atomicAdd(&row[ex[r]], dc[r]);
     }
+    wave_order();
+    float dp[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const v4f v = *reinterpret_cast<const v4f*>(row + (c * LPT + lane) * 8 + 4 * q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dp[c][4 * q + i] = v[i];
+      }
+    wave_order();
     float dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c)
