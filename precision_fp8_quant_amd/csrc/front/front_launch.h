@@ -93,14 +93,25 @@ hipError_t launch_moe_route_backward(const RouteBwdArgs& p, bool bf16, hipStream
 inline int64_t route_lanes(int64_t E) { return E <= 128 ? 8 : E <= 256 ? 16 : E <= 512 ? 32 : 64; }
 // Up to so many tokens (64 of 64 experts, 8 of 1024) one workgroup of 256 threads does it all.
 inline int64_t route_few(int64_t E) { return 2 * 256 / route_lanes(E); }
-// Workgroups of the forward kernel, of 1024 threads beyond that.  One alone also
-// finishes the sums, in up to three turns (384 tokens of 64 experts); more need
-// a second kernel (189 tokens of 9 experts: 9.3 us a call, 11.3 in two kernels).
-// At most 256: each leaves sums to be read (65536 tokens of 64 experts, BF16: 12.1
-// us and 3.8 for the sums, with 512 workgroups 13.1 and 4.4).
+// Threads of a workgroup of the forward kernel, and workgroups.  One alone also
+// finishes the sums, in up to two turns of 1024 threads (256 tokens of 64
+// experts); more need a second kernel (189 tokens of 9 experts: 9.3 us a call,
+// 11.3 in two kernels; with three turns, 384 tokens of 64 experts, 11.4 either way,
+// of which the one kernel is 10.8 and the two are 8).  At most 256: each leaves sums
+// to be read (65536 tokens of 64 experts, BF16: 12.1 us and 3.8 for the sums, with
+// 512 workgroups 13.1 and 4.4).  Their threads: the fewest that take one turn, so
+// that all CUs have some (FP32, 8192 tokens: of 64 experts 5.6 us with 256 threads,
+// 7.3 with 1024; of 256 experts 8.2 with 512, 12.0).
+inline int64_t route_threads(int64_t T, int64_t E) {
+  const int64_t all = T * route_lanes(E);
+  if (T <= route_few(E)) return 256;
+  if (all <= 2 * 1024) return 1024;
+  return all <= 256 * 256 ? 256 : all <= 256 * 512 ? 512 : 1024;
+}
 inline int64_t route_parts(int64_t T, int64_t E) {
-  const int64_t turns = (T * route_lanes(E) + 1023) / 1024;
-  return turns <= 3 ? 1 : turns < 256 ? turns : 256;
+  const int64_t all = T * route_lanes(E), nt = route_threads(T, E);
+  if (all <= 2 * 1024) return 1;
+  return all <= 256 * nt ? (all + nt - 1) / nt : 256;
 }
 // Sums of p, counts, tokens, and the loss's shares of up to 16 workgroups.
 inline int64_t route_workspace(int64_t T, int64_t E) {

@@ -6,18 +6,27 @@
 // LPT lanes share a token and hold its logits in registers, C runs of 8 each
 // (expert (c LPT + lane) 8 + j): one read of the logits serves the softmax and
 // the choice.  The choice goes by the logits themselves, as integers of the same
-// order, so that equal logits are equal: every lane sorts its runs, and each of
-// the k rounds takes the largest of their heads over the lanes, the lowest index
-// where several are, and moves that run up.
+// order, so that equal logits are equal, and lower indexes go first:
+//   4 to 8 experts  keys of a logit and its expert in one integer; every lane sorts
+//                   its runs, and the eights of lanes are merged, level by level.
+//                   BF16 leaves 16 bits for the expert.  FP32 loses 6 to 10 of its
+//                   bits, and where two keys that matter are as close as that (one
+//                   of 2500 tokens of 64 normal logits, of 240 of 256) the wave
+//                   chooses again by
+//   any number      rounds: every lane sorts its runs with all their bits, each of
+//                   the k rounds takes the largest of their heads over the lanes and
+//                   moves that run up.
+// (65536 tokens, merged / by rounds, us: 8 of 64 BF16 9.7 / 11.9, FP32 12.2 / 13.7,
+// 8 of 256 FP32 28.5 / 32.5, 8 of 1000 (16384) 31.2 / 34.8, 4 of 64 BF16 9.2 / 9.6;
+// 2 of 64 a call 12.5 / 12.1, 2 of 1000 34.1 / 31.7.)
 //
 // A lane has the same 8 C experts in all of its workgroup's tokens and sums
 // their p in registers, a wave its groups', a workgroup its waves'; workgroups
 // leave one row of sums and counts each, which a second kernel adds in a fixed
 // order.  With one workgroup it is all one launch.
-// Bound by instructions, more than half of them the choice: 65536 tokens, 8 of 64
-// experts BF16 11.3 us (6.0 without the choice; 16.6 with k scans of all logits
-// instead of sorted runs) and 3.4 for the sums, 8 of 256 FP32 34 us (14).  The gradient
-// is bound by memory: 8 of 256 FP32 30.0 us a call, 4.6 TB/s, 8 of 1000 (16384 tokens) 26.5, 5.0.
+// Bound by instructions, half of them the choice (6 us of the 9.7 are without it),
+// and 3.4 us for the sums.  The gradient is bound by memory: 8 of 256 FP32 30.0 us a
+// call, 4.6 TB/s, 8 of 1000 (16384 tokens) 26.5, 5.0.
 #include "front_launch.h"
 #include "lanes.h"
 #include "row_io.h"
@@ -55,10 +64,13 @@ struct Token {
     for (int c = 0; c < C; ++c) {
       const int e0 = (c * LPT + lane) * 8;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        z[c][j] = e0 + j < cols ? from.raw[c].get(j) : ninf;
-        top = __builtin_fmaxf(top, z[c][j]);
+      for (int j = 0; j < 8; ++j) z[c][j] = from.raw[c].get(j);
+      if (e0 + 8 > cols) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[c][j] = e0 + j < cols ? z[c][j] : ninf;
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, z[c][j]);
     }
     top = lanes_max<LPT>(top);
     counts = top > ninf;
@@ -77,12 +89,14 @@ struct Token {
   __device__ __forceinline__ float term(float v) const { return __builtin_amdgcn_exp2f((v - m) * kLog2e); }
 };
 
-// Integer of the same order as v; both zeros are the same.  0: v is minus
-// infinity or no number.
-__device__ __forceinline__ uint32_t ordered(float v) {
+// Integer of the same order as v; both zeros are the same.  Minus infinity is
+// below kLeastKey.  ordered: 0 for that and for no number.
+constexpr uint32_t kLeastKey = 0x00800000u;
+__device__ __forceinline__ uint32_t in_order(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
-  return v > __uint_as_float(kNegInf) ? u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u) : 0u;
+  return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ uint32_t ordered(float v) { return v > __uint_as_float(kNegInf) ? in_order(v) : 0u; }
 // The logit of a candidate's key; BF16 keys have the expert in their low half.
 __device__ __forceinline__ float logit_of(uint32_t o, float) {
   return __uint_as_float(int32_t(o) < 0 ? o ^ 0x80000000u : ~o);
@@ -98,6 +112,71 @@ __device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
   a = hi;
 }
 
+// Eight in descending order: any, and where the first four and the last four
+// make a bitonic sequence.
+__device__ __forceinline__ void sort8(uint32_t (&key)[8]) {
+  constexpr int net[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                              {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+  for (int i = 0; i < 19; ++i) exchange(key[net[i][0]], key[net[i][1]]);   // odd-even merge sort
+}
+__device__ __forceinline__ void sort8_bitonic(uint32_t (&key)[8]) {
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) exchange(key[i], key[i + d]);
+}
+
+// The eight largest keys of a token in descending order, in every lane of its
+// group.  The larger of a[i] and b[7 - i], for two sorted eights a and b, are
+// the eight largest of both and bitonic: a level is 8 maxima and 12 exchanges.
+template <int LPT, int C>
+__device__ __forceinline__ void best_eight(uint32_t (&run)[C][8]) {
+  static_assert(C <= 2, "runs of a lane");
+  uint32_t(&a)[8] = run[0];
+  sort8(a);
+  uint32_t o[8];
+  const auto join = [&] {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = o[i];
+    sort8_bitonic(a);
+  };
+  if constexpr (C == 2) {
+    sort8(run[1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = a[i] > run[1][7 - i] ? a[i] : run[1][7 - i];
+    join();
+  }
+  const auto level = [&](auto other) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t b = other(a[7 - i]);
+      o[i] = a[i] > b ? a[i] : b;
+    }
+    join();
+  };
+  level([](uint32_t v) { return dpp<0xB1>(v); });  // as in lanes_reduce
+  level([](uint32_t v) { return dpp<0x4E>(v); });
+  level([](uint32_t v) { return dpp<0x141>(v); });
+  if constexpr (LPT >= 16) level([](uint32_t v) { return dpp<0x140>(v); });
+  // The swaps give the lower lanes' key first in both halves: the upper ones have the eight in reverse.
+  const auto swap_level = [&](auto swap) {
+    uint32_t lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const auto v = swap(a[i]);
+      lo[i] = v[0];
+      hi[i] = v[1];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = lo[i] > hi[7 - i] ? lo[i] : hi[7 - i];
+    join();
+  };
+  if constexpr (LPT >= 32) swap_level([](uint32_t v) { return __builtin_amdgcn_permlane16_swap(v, v, false, false); });
+  if constexpr (LPT >= 64) swap_level([](uint32_t v) { return __builtin_amdgcn_permlane32_swap(v, v, false, false); });
+}
+
 // A lane's run of eight candidates, experts e0 .. e0 + 7, in descending order.
 // BF16 leaves room for the index below the logit: a candidate is one integer, no
 // two are equal and a round is one maximum.
@@ -110,10 +189,7 @@ template <> struct Run<uint16_t> {
       const uint32_t o = ordered(z[j]);
       key[j] = o ? (o & 0xFFFF0000u) | uint32_t(0xFFFF - (e0 + j)) : 0u;
     }
-    constexpr int net[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
-                                {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
-#pragma unroll
-    for (int i = 0; i < 19; ++i) exchange(key[net[i][0]], key[net[i][1]]);   // odd-even merge sort
+    sort8(key);
   }
   __device__ __forceinline__ void up(bool taken) {
 #pragma unroll
@@ -229,24 +305,79 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[c][j] = __builtin_fmaf(tok.x[c][j], tok.inv, acc[c][j]);
 
-    Run<T> run[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) run[c].sort(tok.z[c], (c * LPT + lane) * 8);
-    float w[ROUNDS], total = 0.0f;
+    float w[ROUNDS], total = 0.0f;                 // lane j of the group has choice r LPT + j
     int ex[ROUNDS];
+    bool rounds = k < 4 || k > 8;
+    if (!rounds) {
+      const uint32_t low = sizeof(T) == 2 ? 0xFFFFu : uint32_t(EP - 1);   // bits of the key that hold the expert
+      uint32_t key[C][8];
 #pragma unroll
-    for (int r = 0; r < ROUNDS; ++r) {             // lane j of the group keeps choice r LPT + j
-      uint32_t key = 0;
-      ex[r] = -1;
-      for (int j = r * LPT; j < k && j < (r + 1) * LPT; ++j) {
-        const Choice best = choose<LPT, C>(run, lane);
-        if (lane == j - r * LPT) {
-          key = best.key;
-          ex[r] = best.expert;
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          key[c][j] = (in_order(tok.z[c][j]) & ~low) | (low - uint32_t((c * LPT + lane) * 8 + j));
+      uint32_t(&best)[8] = key[0];
+      if constexpr (sizeof(T) == 4) {
+        uint32_t kept[C][8];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) kept[c][j] = key[c][j];
+        best_eight<LPT, C>(key);
+        // Keys that the cut-off bits might order otherwise: neighbours among the eight, and what is next to the last.
+        // (The differences of those above it, and of a key with itself, wrap to the largest integers.)
+        uint32_t gap = 0xFFFFFFFFu;
+#pragma unroll
+        for (int j = 0; j < 7; ++j) gap = min(gap, best[j] - best[j + 1] - 1u);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) gap = min(gap, best[7] - kept[c][j] - 1u);
+        rounds = __ballot(tok.counts && gap < low) != 0;             // uniform over the wave
+        if (rounds) {                              // not with logits that have no such bits, as those that were BF16
+          uint32_t bits = 0;
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bits |= __float_as_uint(tok.z[c][j]);
+          rounds = __ballot((bits & low) != 0) != 0;
         }
+      } else {
+        best_eight<LPT, C>(key);
       }
-      w[r] = key ? tok.term(logit_of(key, T())) * tok.inv : 0.0f;
-      total += w[r];
+      uint32_t mine = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mine = lane == j && j < k ? best[j] : mine;
+      const bool some = mine >= kLeastKey;
+      ex[0] = some ? int(low - (mine & low)) : -1;
+      const float z0 = sizeof(T) == 2 ? logit_of(mine, T()) : some ? load1(logits + t * p.ld_z + ex[0]) : 0.0f;
+      w[0] = some ? tok.term(z0) * tok.inv : 0.0f;
+      total = w[0];
+#pragma unroll
+      for (int r = 1; r < ROUNDS; ++r) {
+        ex[r] = -1;
+        w[r] = 0.0f;
+      }
+    }
+    if (rounds) {
+      Run<T> run[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) run[c].sort(tok.z[c], (c * LPT + lane) * 8);
+      total = 0.0f;
+#pragma unroll
+      for (int r = 0; r < ROUNDS; ++r) {
+        uint32_t key = 0;
+        ex[r] = -1;
+        for (int j = r * LPT; j < k && j < (r + 1) * LPT; ++j) {
+          const Choice best = choose<LPT, C>(run, lane);
+          if (lane == j - r * LPT) {
+            key = best.key;
+            ex[r] = best.expert;
+          }
+        }
+        w[r] = key ? tok.term(logit_of(key, T())) * tok.inv : 0.0f;
+        total += w[r];
+      }
     }
     if (p.renormalize) total = lanes_sum<LPT>(total);
     const float scale = p.renormalize ? (total > 0.0f ? 1.0f / total : 0.0f) : 1.0f;
@@ -443,9 +574,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
 }
 
 // f(LPT, C) for E experts.  The choice is bound by its instructions: two runs a
-// lane share a round's exchanges (65536 tokens, 8 of 256 experts, FP32: 31.6 us
-// with 16 lanes and two runs, 39.1 with 32 and one, 31.3 with 8 and four; 8 of
-// 512 60 / 81; 8 of 128 17.9 / 20.1).  Lanes: route_lanes().
+// lane share a round's exchanges (65536 tokens, 8 of 256 experts by rounds, FP32:
+// 31.6 us with 16 lanes and two runs, 39.1 with 32 and one, 31.3 with 8 and four; 8
+// of 512 60 / 81; 8 of 128 17.9 / 20.1).  Lanes: route_lanes().
 template <typename F>
 hipError_t by_experts(int64_t E, F f) {
   using std::integral_constant;
@@ -470,8 +601,11 @@ template <typename T>
 hipError_t launch_route_t(const RouteArgs& p, hipStream_t st) {
   const int64_t parts = route_parts(p.T, p.E);
   const hipError_t e = by_experts(p.E, [&](auto lpt, auto c) {
-    if (p.T <= route_few(p.E)) hipLaunchKernelGGL((route_kernel<T, lpt(), c(), 256>), dim3(1), dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((route_kernel<T, lpt(), c(), 1024>), dim3(unsigned(parts)), dim3(1024), 0, st, p);
+    const int64_t nt = route_threads(p.T, p.E);
+    const dim3 grid{unsigned(parts)};
+    if (nt == 256) hipLaunchKernelGGL((route_kernel<T, lpt(), c(), 256>), grid, dim3(256), 0, st, p);
+    else if (nt == 512) hipLaunchKernelGGL((route_kernel<T, lpt(), c(), 512>), grid, dim3(512), 0, st, p);
+    else hipLaunchKernelGGL((route_kernel<T, lpt(), c(), 1024>), grid, dim3(1024), 0, st, p);
     return hipGetLastError();
   });
   if (e != hipSuccess || parts == 1) return e;

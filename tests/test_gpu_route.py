@@ -113,6 +113,23 @@ def test_moe_route_ties_and_zeros():
     _check_route(fp8q.moe_route(dev(z), 6), z.astype(np.float64), 6, None, False)
 
 
+@pytest.mark.parametrize("e", [9, 64, 100, 250, 500, 1000])
+@pytest.mark.parametrize("k", [2, 4, 8, 9])
+def test_moe_route_logits_close_to_each_other(e, k):
+    """FP32 logits that differ in their last bits alone, among others that do not, of both signs, and FP32 logits that are
+    BF16 numbers, of which many are equal: in order, the lower index first."""
+    fp8q = require_gpu()
+    rng = np.random.default_rng(e + k)
+    near = (np.float32(1.5).view(np.int32) + rng.integers(0, 3 * e, (60, e))).astype(np.int32).view(np.float32)
+    z = np.concatenate([near, -near, near * np.float32(2.0 ** -140), _logits(60, e, F32, e), _logits(200, e, BF, e)])
+    z[5:180:3] += (rng.random((59, e)) < 0.05).astype(np.float32)               # a few above all the others
+    z[180:200, ::7] = z[180:200, 1::7][:, :1]                                   # equal ones among those that are not
+    _check_route(fp8q.moe_route(_place(z, F32), k, renormalize=True), z.astype(np.float64), k, None, True)
+    for rows in (slice(0, 60), slice(240, 440)):                                # waves of one kind alone
+        part = np.ascontiguousarray(z[rows])
+        _check_route(fp8q.moe_route(_place(part, F32), k), part.astype(np.float64), k, None, False)
+
+
 @pytest.mark.parametrize("case", ["no tokens", "none valid", "all minus infinity"])
 def test_moe_route_where_no_token_counts(case):
     fp8q = require_gpu()
