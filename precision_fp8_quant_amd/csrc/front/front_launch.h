@@ -113,6 +113,11 @@ inline int64_t route_parts(int64_t T, int64_t E) {
   if (all <= 2 * 1024) return 1;
   return all <= 256 * nt ? (all + nt - 1) / nt : 256;
 }
+// Sums, one for each part and expert, up to which one workgroup adds them all and the
+// loss, beyond 64 experts (one launch / two, us a call and in a graph: 1000 tokens of
+// 128 experts, 16128 sums, 14.3 / 17.4 and 9.0 / 9.9; 500 of 512, 32256 sums, 14.1 /
+// 17.8 and 12.2 / 11.0; 4096 of 256, 65536 sums, 15.2 / 17.5 and 13.8 / 11.5).
+constexpr int64_t kRouteFinish = 32768;
 // Sums of p, counts, tokens, and the loss's shares of up to 16 workgroups.
 inline int64_t route_workspace(int64_t T, int64_t E) {
   const int64_t parts = route_parts(T, E);

@@ -424,19 +424,62 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
   }
 }
 
-// Counts, slopes and the loss's share of 64 experts a workgroup: 16 waves take
-// the parts in turn.  `loss`: the loss itself where this is the only workgroup,
-// one word for each otherwise.
-__global__ __launch_bounds__(1024) void route_sums_kernel(RouteArgs p, int64_t parts, float* loss) {
+// The tokens that count in all workgroups of the forward kernel, to each of 1024 threads.
+__device__ __forceinline__ int tokens_of(const RouteArgs& p, int64_t parts, int* wave_n) {
+  int n = 0;
+  for (int64_t b = threadIdx.x; b < parts; b += 1024) n += p.part_n[b];
+  n = int(lanes_reduce<64>(uint32_t(n), [](uint32_t a, uint32_t b) { return a + b; }));
+  if ((threadIdx.x & 63) == 0) wave_n[threadIdx.x >> 6] = n;
+  __syncthreads();
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) n += wave_n[w];
+  return n;
+}
+
+// Counts, slopes and the loss by one workgroup: thread t has expert t mod 2^bits
+// and takes every (1024 / 2^bits)th of the parts.
+__global__ __launch_bounds__(1024) void route_finish_kernel(RouteArgs p, int64_t parts, int bits) {
+  __shared__ float sp[1024];
+  __shared__ int sc[1024];
+  __shared__ int sn[16];
+  __shared__ float part[16];
+  const int t = threadIdx.x, E = int(p.E), e = t & ((1 << bits) - 1), step = 1024 >> bits;
+  float s = 0.0f;
+  int c = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int64_t b = t >> bits; b < parts; b += step) {
+      s += p.part_p[b * E + e];
+      c += p.part_c[b * E + e];
+    }
+  }
+  sp[t] = s;
+  sc[t] = c;
+  const int n = tokens_of(p, parts, sn);           // its barrier is also that of sp and sc
+  float loss = 0.0f;
+  if (t < E) {
+    for (int i = t + (1 << bits); i < 1024; i += 1 << bits) {
+      s += sp[i];
+      c += sc[i];
+    }
+    const float slope = slope_of(p.E, p.k, c, n);
+    p.counts[t] = c;
+    p.slope[t] = slope;
+    loss = slope * s;
+  }
+  loss = row_sum<1024>(loss, part);
+  if (t == 0) p.loss[0] = loss;
+}
+
+// The same for many experts, 64 a workgroup, whose 16 waves take the parts in
+// turn; a share of the loss each.
+__global__ __launch_bounds__(1024) void route_sums_kernel(RouteArgs p, int64_t parts) {
   __shared__ float sp[16][64];
   __shared__ int sc[16][64];
   __shared__ int sn[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t e = int64_t(blockIdx.x) * 64 + lane;
-  int n = 0;
-  for (int64_t b = threadIdx.x; b < parts; b += 1024) n += p.part_n[b];
-  n = int(lanes_reduce<64>(uint32_t(n), [](uint32_t a, uint32_t b) { return a + b; }));
-  if (lane == 0) sn[wave] = n;
   float s = 0.0f;
   int c = 0;
   if (e < p.E) {
@@ -448,12 +491,10 @@ __global__ __launch_bounds__(1024) void route_sums_kernel(RouteArgs p, int64_t p
   }
   sp[wave][lane] = s;
   sc[wave][lane] = c;
-  __syncthreads();
+  const int n = tokens_of(p, parts, sn);           // its barrier is also that of sp and sc
   if (wave != 0) return;
-  n = sn[0];
 #pragma unroll
   for (int w = 1; w < 16; ++w) {
-    n += sn[w];
     s += sp[w][lane];
     c += sc[w][lane];
   }
@@ -464,7 +505,7 @@ __global__ __launch_bounds__(1024) void route_sums_kernel(RouteArgs p, int64_t p
     p.slope[e] = slope;
   }
   const float l = lanes_sum<64>(slope * s);
-  if (lane == 0) loss[blockIdx.x] = l;
+  if (lane == 0) p.part_l[blockIdx.x] = l;
 }
 
 __global__ __launch_bounds__(64) void route_loss_kernel(const float* part, int n, float* loss) {
@@ -609,10 +650,16 @@ hipError_t launch_route_t(const RouteArgs& p, hipStream_t st) {
     return hipGetLastError();
   });
   if (e != hipSuccess || parts == 1) return e;
+  if (p.E <= 64 || parts * p.E <= kRouteFinish) {
+    int bits = 6;
+    while ((int64_t(1) << bits) < p.E) ++bits;
+    hipLaunchKernelGGL(route_finish_kernel, dim3(1), dim3(1024), 0, st, p, parts, bits);
+    return hipGetLastError();
+  }
   const unsigned blocks = unsigned((p.E + 63) / 64);
-  hipLaunchKernelGGL(route_sums_kernel, dim3(blocks), dim3(1024), 0, st, p, parts, blocks == 1 ? p.loss : p.part_l);
+  hipLaunchKernelGGL(route_sums_kernel, dim3(blocks), dim3(1024), 0, st, p, parts);
   const hipError_t e2 = hipGetLastError();
-  if (e2 != hipSuccess || blocks == 1) return e2;
+  if (e2 != hipSuccess) return e2;
   hipLaunchKernelGGL(route_loss_kernel, dim3(1), dim3(64), 0, st, p.part_l, int(blocks), p.loss);
   return hipGetLastError();
 }

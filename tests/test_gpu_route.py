@@ -77,6 +77,20 @@ def test_moe_route(t, e, k, renormalize, dtype):
     _check_route(fp8q.moe_route(_place(z, dtype), k, renormalize=renormalize), z.astype(np.float64), k, None, renormalize)
 
 
+@pytest.mark.parametrize("e, lanes", [(64, 8), (120, 8), (256, 16), (500, 32), (1000, 64)])
+@pytest.mark.parametrize("all_lanes, dtype", [(1 << 11, F32), (1 << 12, BF), ((1 << 16) - 64, F32), ((1 << 16) + 64, BF),
+                                              ((1 << 17) + 64, F32), ((1 << 18) + 64, BF)])
+def test_moe_route_in_workgroups_of_every_size(all_lanes, dtype, e, lanes):
+    """One workgroup, several of 256, 512 and 1024 threads, of these in more than one turn; sums by one workgroup and by
+    several."""
+    fp8q = require_gpu()
+    t = all_lanes // lanes
+    z = _logits(t, e, dtype, t + e)
+    valid = (np.random.default_rng(t).random(t) < 0.9).astype(np.uint8)
+    k = 8 if t % 3 else 3
+    _check_route(fp8q.moe_route(_place(z, dtype), k, valid=dev(valid)), z.astype(np.float64), k, valid, False)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("t, e, k", [(16, 64, 8), (300, 64, 4), (77, 130, 8), (40, 600, 3)])
 def test_moe_route_masks(t, e, k, dtype):
