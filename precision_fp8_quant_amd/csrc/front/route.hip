@@ -25,8 +25,8 @@
 // leave one row of sums and counts each, which a second kernel adds in a fixed
 // order.  With one workgroup it is all one launch.
 // Bound by instructions, half of them the choice (6 us of the 9.7 are without it),
-// and 3.4 us for the sums.  The gradient is bound by memory: 8 of 256 FP32 30.0 us a
-// call, 4.6 TB/s, 8 of 1000 (16384 tokens) 26.5, 5.0.
+// and 3.8 us for the sums.  The gradient is bound by memory: 8 of 256 FP32 27.5 us a
+// call, 5.0 TB/s, 8 of 1000 (16384 tokens) 26.5, 5.0.
 #include "front_launch.h"
 #include "lanes.h"
 #include "row_io.h"
