@@ -37,7 +37,7 @@ def _load_native():
             return _ffn_call
         why = f"built for torch {_ffn_call.torch_version}, this is {torch.__version__}"
     warnings.warn(f"{_NATIVE_PATH} is not used: {why}. Rebuild it with __graft_entry__.build(); until then calls of the "
-                  "gated feed-forward operators take more host time", RuntimeWarning, stacklevel=3)
+                  "gated feed-forward, norm, routing and dispatch operators take more host time", RuntimeWarning, stacklevel=3)
     return None
 
 

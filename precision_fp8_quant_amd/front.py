@@ -51,7 +51,8 @@ _i32 = torch.int32
 
 # The usual call (new outputs, current device and stream) is made by csrc/front/binding.cpp in one step; it answers None
 # for anything else, and an int where the C ABI refuses.  What follows it here takes every call, and says what is wrong
-# with one.
+# with one.  (A module that was built from csrc/ffn/ alone has no such functions.)
+_native = _native if hasattr(_native, "fp8_rmsnorm") else None
 
 
 def _code(t, name):
