@@ -6,14 +6,14 @@
 // does not depend on timing.  A wave takes a chunk of slots 64 at a time: lanes
 // of equal experts find each other by one ballot per bit of the expert, a
 // lane's place is the expert's running count plus its equals in lower lanes.
-//   up to 1024 slots   no plan of its own: every workgroup of the one kernel finds
+//   up to 4096 slots   no plan of its own: every workgroup of the one kernel finds
 //                      the experts' tiles and its tile's tokens for itself
 //   up to 8192         one workgroup: counts of its 16 waves' chunks, their
 //                      prefix sums and the tile map, the rows
 //   beyond             two kernels of up to 128 workgroups of 16 chunks: the counts
 //                      of chunks and workgroups; then the rows, every workgroup
 //                      summing the others' counts for itself
-// Then (beyond 1024 slots) one kernel moves codes and scales: a token's row is
+// Then (beyond 4096 slots) one kernel moves codes and scales: a token's row is
 // read once and written to its k places; scales, which lie transposed, are
 // written in runs of a tile's 128 rows, with the padding rows of the tile.
 // Bound by memory: 65536 rows of 7168 codes move in 117 us, 5.0 TB/s (a large copy:
@@ -283,17 +283,15 @@ __global__ __launch_bounds__(256) void move_kernel(DispatchArgs p, int64_t tile_
 // finds the expert of its tile and lists the tile's slots in their order; the
 // first piece of a tile also writes its part of the maps.
 // ---------------------------------------------------------------------------
-constexpr int kOneLaunch = int(kDispatchOneLaunch);
-
+template <int STEPS>                                // slots of a thread; a wave's are consecutive
 __global__ __launch_bounds__(256) void dispatch_few_kernel(DispatchArgs p, int64_t pieces, int64_t units) {
-  constexpr int STEPS = kOneLaunch / 256;          // slots of a thread; a wave's are consecutive
   constexpr int PER = int(kMaxExperts) / 256;      // experts of a thread
   __shared__ int count[kMaxExperts];
   __shared__ int token[128], slot_of[128];
   __shared__ int wave_sum[4];
   __shared__ int tile_expert, tile_skip;           // the tile's expert (-1: not in use), its slots in earlier tiles
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, E = int(p.E), slots = int(p.T * p.k), k = int(p.k);
-  const int slot0 = wave * (kOneLaunch / 4) + lane;
+  const int slot0 = wave * (STEPS * 64) + lane;
   int e[STEPS];
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
@@ -405,7 +403,9 @@ hipError_t launch_moe_dispatch(const DispatchArgs& p, hipStream_t st) {
   const int64_t slots = p.T * p.k;
   if (slots <= kDispatchOneLaunch) {
     const int64_t pieces = p.D > 1024 ? (p.D + 1023) / 1024 : 1, units = p.M_total / 128 * pieces;
-    hipLaunchKernelGGL(dispatch_few_kernel, dim3(grid_of(units, 256)), dim3(256), 0, st, p, pieces, units);
+    const dim3 grid(grid_of(units, 256));
+    if (slots <= 1024) hipLaunchKernelGGL(dispatch_few_kernel<4>, grid, dim3(256), 0, st, p, pieces, units);
+    else hipLaunchKernelGGL(dispatch_few_kernel<kDispatchOneLaunch / 256>, grid, dim3(256), 0, st, p, pieces, units);
     return hipGetLastError();
   }
   const unsigned groups = unsigned(dispatch_groups(slots));

@@ -137,9 +137,11 @@ struct DispatchArgs {
 };
 hipError_t launch_moe_dispatch(const DispatchArgs& p, hipStream_t st);
 
-// Slots that every workgroup counts for itself, in one launch with the rest
-// (16 tokens of 8 experts, 7168 codes: 16.3 us a call in two launches, 11.8 in one).
-constexpr int64_t kDispatchOneLaunch = 1024;
+// Slots that every workgroup counts for itself, in one launch with the rest (us a
+// call, in one launch / in two: 16 tokens of 8 experts, 7168 codes, 11.8 / 16.3; 512
+// of 8 of 64, 7168 codes 18.0 / 19.8, 2048 codes 13.6 / 16.8; 1024 of 8 of 64, 7168
+// codes 40.1 / 29.0, 2048 codes 17.5 / 20.9).
+constexpr int64_t kDispatchOneLaunch = 4096;
 // Slots whose ranks one workgroup alone finds.
 constexpr int64_t kDispatchAlone = 8192;
 

@@ -271,7 +271,8 @@ def _check_dispatch(fp8q, experts, e, d, seed, extra=0):
 @pytest.mark.parametrize("t, k, e, d", [(1, 1, 1, 128), (1, 8, 64, 1152), (16, 8, 64, 256), (37, 3, 5, 1024), (300, 2, 7, 384), (1024, 8, 64, 128),
                                         (1023, 8, 200, 128), (1025, 8, 64, 128), (2500, 4, 1000, 128), (900, 32, 33, 128),
                                         (5000, 2, 3, 256), (1, 32, 1024, 2176), (9000, 1, 1, 128), (1024, 1, 3, 1152),
-                                        (1025, 1, 3, 1152), (512, 2, 1024, 128), (33, 31, 1, 2048)])
+                                        (1025, 1, 3, 1152), (512, 2, 1024, 128), (33, 31, 1, 2048),
+                                        (4096, 1, 7, 1152), (1366, 3, 9, 128), (2048, 2, 1000, 256), (8192, 1, 64, 128)])
 def test_dispatch(t, k, e, d):
     fp8q = require_gpu()
     rng = np.random.default_rng(t + e)
@@ -280,7 +281,7 @@ def test_dispatch(t, k, e, d):
     _check_dispatch(fp8q, experts, e, d, seed=t, extra=128 * (t % 3))
 
 
-@pytest.mark.parametrize("t, k", [(100, 8), (200, 8), (3000, 8)])
+@pytest.mark.parametrize("t, k", [(100, 8), (200, 8), (600, 8), (3000, 8)])
 def test_dispatch_choices_outside_the_experts(t, k):
     """-1, and anything else outside the range, gets no row; an expert without rows no tile."""
     fp8q = require_gpu()
