@@ -38,6 +38,9 @@ __device__ __forceinline__ float max_abs8(const float (&v)[8]) {
 template <typename T, typename W, int TPR, int R, int OUT, bool ONCE>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(NormArgs p) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
+  // With four runs of 1024 threads the registers hold no weight before the sum (512x32768 FP32, us: 21.6, with it, which
+  // spills, 30.2; with a residual 50 and 67).
+  constexpr bool LATE = TPR * R > 2048;
   __shared__ float part[2][NT / 64];
   const int t = threadIdx.x & (TPR - 1);
   const T* __restrict__ x = static_cast<const T*>(p.x);
@@ -58,7 +61,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(NormArgs
 #pragma unroll
       for (int i = 0; i < R; ++i) load_raw<ONCE>(rr[i], r + row * p.ld_r, (i * TPR + t) * 8, D);
     }
-    if constexpr (OUT != kOutNone) {
+    if constexpr (OUT != kOutNone && !LATE) {
 #pragma unroll
       for (int i = 0; i < R; ++i) load_raw(wr[i], weight, (i * TPR + t) * 8, D);
     }
@@ -88,6 +91,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(NormArgs
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int col = (i * TPR + t) * 8;
+        if constexpr (LATE) load_raw(wr[i], weight, col, D);
         trim(wr[i], col, D);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * wr[i].get(j);

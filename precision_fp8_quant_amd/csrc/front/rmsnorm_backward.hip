@@ -22,9 +22,11 @@ namespace {
 template <typename T, typename W, int TPR, int R, bool ONCE>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel(NormBwdArgs p) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
-  // With four runs the registers hold no more than dy and h: the sums of dw are in LDS, each thread's its own
-  // (2048x32768 with dh, us: BF16 117, in registers, which spill, 194; FP32, which spills still, 390 and 566).
+  // With four runs the registers hold no more than dy and h: the sums of dw are in LDS, each thread's its own.  In FP32
+  // they hold dy alone, and h is read again from the caches.  (2048x32768 with dh, us: BF16 114, with the sums in
+  // registers, which spill, 194; FP32 343, with h in registers 390, the sums too 566.)
   constexpr bool LATE = R > 2;
+  constexpr bool AGAIN = LATE && sizeof(T) == 4;
   __shared__ v4f far[LATE ? 2 * R : 1][LATE ? TPR : 1];
   __shared__ float part[2][NT / 64];
   const int t = threadIdx.x & (TPR - 1);
@@ -51,11 +53,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
   for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < p.M; row0 += int64_t(gridDim.x) * RPB) {
     const int64_t row = row0 + threadIdx.x / TPR;
     const int D = row < p.M ? int(p.D) : 0;
-    Row8<T> yr[R], hr[R], er[R];
+    Row8<T> yr[R], hr[AGAIN ? 1 : R], er[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) load_raw<ONCE>(yr[i], dy + row * p.ld_dy, (i * TPR + t) * 8, D);
+    if constexpr (!AGAIN) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) load_raw<ONCE>(hr[i], h + row * p.ld_h, (i * TPR + t) * 8, D);
+      for (int i = 0; i < R; ++i) load_raw<ONCE>(hr[i], h + row * p.ld_h, (i * TPR + t) * 8, D);
+    }
     if (!LATE && dh) {
 #pragma unroll
       for (int i = 0; i < R; ++i) load_raw<ONCE>(er[i], dh + row * p.ld_dh, (i * TPR + t) * 8, D);
@@ -66,13 +70,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
     for (int i = 0; i < R; ++i) {
       const int col = (i * TPR + t) * 8;
       if constexpr (LATE) load_raw(wr[i], weight, col, D);
+      Row8<T>& hi = hr[AGAIN ? 0 : i];
+      if constexpr (AGAIN) load_raw(hi, h + row * p.ld_h, col, D);
       trim(yr[i], col, D);
-      trim(hr[i], col, D);
+      trim(hi, col, D);
       trim(wr[i], col, int(p.D));
       float z[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        z[j] = yr[i].get(j) * (hr[i].get(j) * rs);
+        z[j] = yr[i].get(j) * (hi.get(j) * rs);
         if constexpr (!LATE) acc[i][j] += z[j];
         sum = __builtin_fmaf(z[j], wr[i].get(j), sum);
       }
@@ -87,7 +93,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       yr[i].opaque();                              // unpacked again rather than held unpacked
-      hr[i].opaque();
+      Row8<T>& hi = hr[AGAIN ? 0 : i];
+      if constexpr (AGAIN) load_raw(hi, h + row * p.ld_h, (i * TPR + t) * 8, D);
+      else hi.opaque();
       if constexpr (LATE) {
         load_raw(wr[i], weight, (i * TPR + t) * 8, D);
         if (dh) load_raw<ONCE>(er[i], dh + row * p.ld_dh, (i * TPR + t) * 8, D);
@@ -95,7 +103,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[j] = rs * __builtin_fmaf(-(hr[i].get(j) * rs), c, yr[i].get(j) * wr[i].get(j));
+        v[j] = rs * __builtin_fmaf(-(hi.get(j) * rs), c, yr[i].get(j) * wr[i].get(j));
         if (dh) v[j] += er[i].get(j);
       }
       store_raw(dx + row * p.ld_dx, (i * TPR + t) * 8, D, v);
