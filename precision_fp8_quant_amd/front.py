@@ -236,9 +236,10 @@ def moe_route(logits, k, valid=None, renormalize=False, weights=None, experts=No
     (t, e), dev, code, k = logits.shape, logits.device, _code(logits, "logits"), int(k)
     if valid is not None:
         _expect(valid, "valid", torch.bool if valid.dtype == torch.bool else torch.uint8, (t,), dev, dense=True)
+    places = max(min(k, e + 1), 0)                 # more than there are experts is the entry point's to refuse
     with _outputs_on(stream, dev, None):
-        weights = _packed(weights, "weights", _f32, (t, max(k, 0)), dev)
-        experts = _packed(experts, "experts", _i32, (t, max(k, 0)), dev)
+        weights = _packed(weights, "weights", _f32, (t, places), dev)
+        experts = _packed(experts, "experts", _i32, (t, places), dev)
         counts = _packed(counts, "counts", _i32, (e,), dev)
         loss = _packed(loss, "loss", _f32, (1,), dev)
         slope = _packed(slope, "slope", _f32, (e,), dev)

@@ -383,3 +383,11 @@ def test_route_and_dispatch_refusals():
     with pytest.raises(fp8q.Fp8qError) as err:                                 # too few rows for 8 slots of 8 experts
         fp8q.fp8_moe_dispatch(i(4, 2), u(4, 128), f(1, 4), 8, a=u(896, 128))
     assert err.value.status == fp8q.ERR_SHAPE
+
+
+def test_route_refuses_more_experts_than_memory_holds():
+    fp8q = require_gpu()
+    for k in (300, 1 << 40):
+        with pytest.raises(fp8q.Fp8qError) as err:
+            fp8q.moe_route(torch.zeros((4, 8), device="cuda"), k)
+        assert err.value.status == fp8q.ERR_SHAPE
