@@ -71,8 +71,8 @@ __device__ __forceinline__ float groups_sum(float v) {
   return v;
 }
 
-// Sum over the TPR threads that share a row: a group of lanes, a wave, or the
-// whole workgroup through `part`, one word per wave.  With TPR > 64 every
+// Sum over the TPR threads that share a row: a group of lanes, a wave, or TPR / 64
+// waves of the workgroup through `part`, one word per wave.  With TPR > 64 every
 // thread of the workgroup calls it; `part` may be written again after the next
 // barrier.
 template <int TPR>
@@ -81,9 +81,10 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   if constexpr (TPR > 64) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = part[0];
+    const float* mine = part + threadIdx.x / TPR * (TPR / 64);
+    v = mine[0];
 #pragma unroll
-    for (int w = 1; w < TPR / 64; ++w) v += part[w];
+    for (int w = 1; w < TPR / 64; ++w) v += mine[w];
   }
   return v;
 }

@@ -19,9 +19,9 @@ namespace fp8q {
 namespace {
 
 // ONCE: dy, h and dh past the caches.
-template <typename T, typename W, int TPR, int R, bool ONCE>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel(NormBwdArgs p) {
-  constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
+template <typename T, typename W, int TPR, int R, int NT, bool ONCE>
+__global__ __launch_bounds__(NT) void rmsnorm_backward_kernel(NormBwdArgs p) {
+  constexpr int RPB = NT / TPR;                    // rows at a time
   // With four runs the registers hold no more than dy and h: the sums of dw are in LDS, each thread's its own.  In FP32
   // they hold dy alone, and h is read again from the caches.  (2048x32768 with dh, us: BF16 114, with the sums in
   // registers, which spill, 194; FP32 343, with h in registers 390, the sums too 566.)
@@ -161,26 +161,33 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restri
   }
 }
 
-template <typename T, typename W, int TPR, int R>
+template <typename T, typename W, int TPR, int R, int NT>
 void launch_rows(const NormBwdArgs& p, int64_t parts, hipStream_t st) {
-  constexpr int NT = TPR < 256 ? 256 : TPR;
-  if (p.once) hipLaunchKernelGGL((rmsnorm_backward_kernel<T, W, TPR, R, true>), dim3(unsigned(parts)), dim3(NT), 0, st, p);
-  else hipLaunchKernelGGL((rmsnorm_backward_kernel<T, W, TPR, R, false>), dim3(unsigned(parts)), dim3(NT), 0, st, p);
+  const dim3 grid{unsigned(parts)};
+  if (p.once) hipLaunchKernelGGL((rmsnorm_backward_kernel<T, W, TPR, R, NT, true>), grid, dim3(NT), 0, st, p);
+  else hipLaunchKernelGGL((rmsnorm_backward_kernel<T, W, TPR, R, NT, false>), grid, dim3(NT), 0, st, p);
 }
 
 template <typename T, typename W>
 hipError_t launch(const NormBwdArgs& p, hipStream_t st) {
-  const int64_t parts = norm_bwd_parts(p.M, p.D);  // which counts on the rows of a workgroup here
+  int64_t parts = norm_bwd_parts(p.M, p.D);        // which counts on the rows of a workgroup here
+  // BF16 rows of 1025 to 2048 channels, more than 512 of them: four at a time, in a quarter of the workgroups (with dh,
+  // us in a graph, four / one: 1511x2048 9.7 / 11.4, 8192x2048 25.6 / 27.5, 32768x1536 78 / 93; 128x2048 5.7 / 5.2;
+  // FP32 1511x2048 13.3 / 14.5, 8192x2048 55.9 / 52.7, 32768x2048 198 / 188).
+  const bool four = sizeof(T) == 2 && p.D > 1024 && p.D <= 2048 && p.M > 512;
+  if (four) parts = p.M < 1024 ? (p.M + 3) / 4 : 256;   // never more than norm_bwd_parts says
   if (parts > 0) {
-    if (p.D <= 128) launch_rows<T, W, 16, 1>(p, parts, st);
-    else if (p.D <= 256) launch_rows<T, W, 16, 2>(p, parts, st);
-    else if (p.D <= 512) launch_rows<T, W, 64, 1>(p, parts, st);
-    else if (p.D <= 1024) launch_rows<T, W, 64, 2>(p, parts, st);
-    else if (p.D <= 2048) launch_rows<T, W, 256, 1>(p, parts, st);
-    else if (p.D <= 4096) launch_rows<T, W, 512, 1>(p, parts, st);
-    else if (p.D <= 8192) launch_rows<T, W, 1024, 1>(p, parts, st);
-    else if (p.D <= 16384) launch_rows<T, W, 1024, 2>(p, parts, st);
-    else launch_rows<T, W, 1024, 4>(p, parts, st);
+    if (four) {
+      if constexpr (sizeof(T) == 2) launch_rows<T, W, 256, 1, 1024>(p, parts, st);
+    } else if (p.D <= 128) launch_rows<T, W, 16, 1, 256>(p, parts, st);
+    else if (p.D <= 256) launch_rows<T, W, 16, 2, 256>(p, parts, st);
+    else if (p.D <= 512) launch_rows<T, W, 64, 1, 256>(p, parts, st);
+    else if (p.D <= 1024) launch_rows<T, W, 64, 2, 256>(p, parts, st);
+    else if (p.D <= 2048) launch_rows<T, W, 256, 1, 256>(p, parts, st);
+    else if (p.D <= 4096) launch_rows<T, W, 512, 1, 512>(p, parts, st);
+    else if (p.D <= 8192) launch_rows<T, W, 1024, 1, 1024>(p, parts, st);
+    else if (p.D <= 16384) launch_rows<T, W, 1024, 2, 1024>(p, parts, st);
+    else launch_rows<T, W, 1024, 4, 1024>(p, parts, st);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -208,7 +208,7 @@ def test_norm_empty():
 # rmsnorm_backward
 # ---------------------------------------------------------------------------
 BWD = [(1, 1), (3, 7), (2, 129), (5000, 250), (130, 333), (9, 512), (70, 1023), (33, 2047), (20, 4097), (700, 2048), (5, 7168), (3, 8191),
-       (2, 16383), (300, 8200), (2, 32767), (1, 32768), (2100, 64), (4500, 520)]
+       (2, 16383), (300, 8200), (2, 32767), (1, 32768), (2100, 64), (4500, 520), (513, 1500), (1030, 1032)]
 
 
 @pytest.mark.parametrize("dtype, wdtype", [(BF, BF), (F32, F32), (BF, F32), (F32, BF)])
