@@ -130,15 +130,15 @@ int rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h,
   if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype) || !flag_ok(accumulate)) return FP8Q_ERR_ARG;
   if (M < 0 || D < 0) return FP8Q_ERR_SHAPE;
   if (D == 0) return FP8Q_OK;
-  const bool rows = M > 0;
-  if (!dw || (rows && (!dy || !h || !weight || !rstd || !dx || !workspace))) return FP8Q_ERR_NULL;
+  const bool rows = M > 0, wide = D > fp8q::kMaxNormD;     // wide: no workspace has a size
+  if (!dw || (rows && (!dy || !h || !weight || !rstd || !dx || (!workspace && !wide)))) return FP8Q_ERR_NULL;
   if (rows && (ld_dy < D || ld_h < D || ld_dx < D || (dh && ld_dh < D))) return FP8Q_ERR_SHAPE;
   const int64_t xs = dtype_size(x_dtype), ws = dtype_size(w_dtype);
   if (!aligned16(dw) || (rows && (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(rstd) ||
                                   !aligned16(dx) || !aligned16(workspace) || !ld_ok(ld_dy, xs) || !ld_ok(ld_h, xs) ||
                                   !ld_ok(ld_dx, xs) || (dh && (!aligned16(dh) || !ld_ok(ld_dh, xs))))))
     return FP8Q_ERR_ALIGN;
-  if (D > fp8q::kMaxNormD) return FP8Q_ERR_UNSUPPORTED;
+  if (wide) return FP8Q_ERR_UNSUPPORTED;
   const int64_t m1 = rows ? 1 : 0;
   const Range outs[3] = {matrix(dx, M, D, ld_dx, xs), packed(dw, D, 4),
                          packed(workspace, m1 * fp8q::norm_bwd_workspace(M, D), 1)};

@@ -114,6 +114,14 @@ def test_rmsnorm_backward_validation(want, kw):
     assert _bwd(**kw) == getattr(fp8q, want), kw
 
 
+@pytest.mark.parametrize("m", [0, 200])
+def test_rmsnorm_backward_beyond_its_widest_row(m):
+    """There is no workspace to ask for there: without one the refusal is that of the width."""
+    kw = dict(m=m, d=32769, **{n: 32772 for n in ("lddy", "ldh", "lddh", "lddx")})
+    assert fp8q.lib.fp8q_rmsnorm_backward_workspace(m, 32769) == -1
+    assert _bwd(ws=None, **kw) == fp8q.ERR_UNSUPPORTED and _bwd(**kw) == fp8q.ERR_UNSUPPORTED
+
+
 def _route(**kw):
     v = dict(z=X, ldz=64, dt=fp8q.F32, t=500, e=60, k=8, valid=R, renorm=0, w=W, ex=H, c=S, loss=Y, slope=Q, ws=WS)
     v.update(kw)

@@ -317,6 +317,16 @@ def test_norm_refusals():
     assert e.value.status == fp8q.ERR_ALIAS
 
 
+@pytest.mark.parametrize("given", [False, True])
+def test_rmsnorm_backward_refuses_rows_beyond_the_widest(given):
+    """The native call (no output given) and the other one alike."""
+    fp8q = require_gpu()
+    x, w = torch.ones((2, 32776), device="cuda")[:, :32769], torch.ones(32769, device="cuda")
+    with pytest.raises(fp8q.Fp8qError) as e:
+        fp8q.rmsnorm_backward(x, x, w, torch.ones(2, device="cuda"), **(dict(dw=torch.zeros_like(w)) if given else {}))
+    assert e.value.status == fp8q.ERR_UNSUPPORTED
+
+
 # ---------------------------------------------------------------------------
 # Inputs of more than 96 MB are read past the caches, by kernels of their own
 # ---------------------------------------------------------------------------
