@@ -177,6 +177,9 @@ PyObject* moe_route_call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const int64_t t = z->size(0), e = z->size(1);
   FP8Q_NONE_UNLESS(!valid || ((valid->scalar_type() == at::kBool || valid->scalar_type() == at::kByte) &&
                               valid->device() == dev && valid->dim() == 1 && valid->size(0) == t && valid->is_contiguous()));
+  // sizes are refused before memory is asked for: the C ABI looks at pointers behind them
+  FP8Q_NONE_UNLESS(moe_route(nullptr, ld, code, t, e, k, nullptr, renormalize, nullptr, nullptr, nullptr, nullptr, nullptr,
+                             nullptr, nullptr) == FP8Q_ERR_NULL);
   const int64_t bytes = fp8q_moe_route_workspace(t, e);
   at::Tensor w, ex, counts, loss, slope, work;
   int status;

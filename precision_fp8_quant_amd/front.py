@@ -16,7 +16,7 @@ import ctypes
 
 import torch
 
-from . import MAXABS, _cdiv, _codes, _expect, _i64, _int, _outputs_on, _ptr, _rowmajor, lib
+from . import ERR_NULL, MAXABS, _cdiv, _check, _codes, _expect, _i64, _int, _outputs_on, _ptr, _rowmajor, lib
 from .ffn import _CODE, _call, _done, _f32, _i8, _ld, _native, _out
 
 _f = ctypes.c_float
@@ -236,10 +236,13 @@ def moe_route(logits, k, valid=None, renormalize=False, weights=None, experts=No
     (t, e), dev, code, k = logits.shape, logits.device, _code(logits, "logits"), int(k)
     if valid is not None:
         _expect(valid, "valid", torch.bool if valid.dtype == torch.bool else torch.uint8, (t,), dev, dense=True)
-    places = max(min(k, e + 1), 0)                 # more than there are experts is the entry point's to refuse
+    # sizes are the entry point's to refuse, before memory is asked for: it looks at pointers behind them
+    status = lib.moe_route(None, _ld(logits), code, t, e, k, None, 0, None, None, None, None, None, None, None)
+    if status != ERR_NULL:
+        _check(status)
     with _outputs_on(stream, dev, None):
-        weights = _packed(weights, "weights", _f32, (t, places), dev)
-        experts = _packed(experts, "experts", _i32, (t, places), dev)
+        weights = _packed(weights, "weights", _f32, (t, k), dev)
+        experts = _packed(experts, "experts", _i32, (t, k), dev)
         counts = _packed(counts, "counts", _i32, (e,), dev)
         loss = _packed(loss, "loss", _f32, (1,), dev)
         slope = _packed(slope, "slope", _f32, (e,), dev)

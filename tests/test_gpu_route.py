@@ -391,3 +391,21 @@ def test_route_refuses_more_experts_than_memory_holds():
         with pytest.raises(fp8q.Fp8qError) as err:
             fp8q.moe_route(torch.zeros((4, 8), device="cuda"), k)
         assert err.value.status == fp8q.ERR_SHAPE
+
+
+@pytest.mark.parametrize("e, k", [(64, 65), (64, 200), (64, 255), (64, 40), (8, 9), (1024, 33), (1032, 8)])
+@pytest.mark.parametrize("given", [False, True])
+def test_route_refuses_before_memory_is_asked_for(e, k, given):
+    """The native call (no output given) and the other one alike: more places than there are experts or than are
+    supported, more experts than are."""
+    fp8q = require_gpu()
+    t = 1 << 16
+    z = torch.zeros((t, e), dtype=BF, device="cuda")
+    kw = dict(loss=torch.zeros(1, device="cuda")) if given else {}
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    held = torch.cuda.memory_allocated()
+    with pytest.raises(fp8q.Fp8qError) as err:
+        fp8q.moe_route(z, k, **kw)
+    assert err.value.status == (fp8q.ERR_SHAPE if k > e else fp8q.ERR_UNSUPPORTED)
+    assert torch.cuda.max_memory_allocated() == held
