@@ -10,9 +10,9 @@
 //   4 to 8 experts  keys of a logit and its expert in one integer; every lane sorts
 //                   its runs, and the eights of lanes are merged, level by level.
 //                   BF16 leaves 16 bits for the expert.  FP32 loses 6 to 10 of its
-//                   bits, and where two keys that matter are as close as that (one
-//                   of 2500 tokens of 64 normal logits, of 240 of 256) the wave
-//                   chooses again by
+//                   bits, and where this could matter to the choice (route_choice.h;
+//                   8 of normal logits: one of 4200 tokens of 64, one of 500 of 256)
+//                   the wave chooses again by
 //   any number      rounds: every lane sorts its runs with all their bits, each of
 //                   the k rounds takes the largest of their heads over the lanes and
 //                   moves that run up.
@@ -29,6 +29,7 @@
 // call, 5.0 TB/s, 8 of 1000 (16384 tokens) 26.5, 5.0.
 #include "front_launch.h"
 #include "lanes.h"
+#include "route_choice.h"
 #include "row_io.h"
 
 #include <type_traits>
@@ -89,13 +90,7 @@ struct Token {
   __device__ __forceinline__ float term(float v) const { return __builtin_amdgcn_exp2f((v - m) * kLog2e); }
 };
 
-// Integer of the same order as v; both zeros are the same.  Minus infinity is
-// below kLeastKey.  ordered: 0 for that and for no number.
-constexpr uint32_t kLeastKey = 0x00800000u;
-__device__ __forceinline__ uint32_t in_order(float v) {
-  const uint32_t u = __float_as_uint(v + 0.0f);
-  return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
-}
+// in_order(), and 0 for minus infinity and for no number.
 __device__ __forceinline__ uint32_t ordered(float v) { return v > __uint_as_float(kNegInf) ? in_order(v) : 0u; }
 // The logit of a candidate's key; BF16 keys have the expert in their low half.
 __device__ __forceinline__ float logit_of(uint32_t o, float) {
@@ -315,32 +310,28 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteArgs p) {
       for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          key[c][j] = (in_order(tok.z[c][j]) & ~low) | (low - uint32_t((c * LPT + lane) * 8 + j));
+          key[c][j] = key_of(in_order(tok.z[c][j]), (c * LPT + lane) * 8 + j, low);
       uint32_t(&best)[8] = key[0];
       if constexpr (sizeof(T) == 4) {
-        uint32_t kept[C][8];
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) kept[c][j] = key[c][j];
         best_eight<LPT, C>(key);
-        // Keys that the cut-off bits might order otherwise: neighbours among the eight, and what is next to the last.
-        // (The differences of those above it, and of a key with itself, wrap to the largest integers.)
-        uint32_t gap = 0xFFFFFFFFu;
+        bool behind = false;
+        if (k == 8) {
+          const float least = least_of(best[7], low);
+          uint32_t n8 = 0;
 #pragma unroll
-        for (int j = 0; j < 7; ++j) gap = min(gap, best[j] - best[j + 1] - 1u);
+          for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) gap = min(gap, best[7] - kept[c][j] - 1u);
-        rounds = __ballot(tok.counts && gap < low) != 0;             // uniform over the wave
+            for (int j = 0; j < 8; ++j) n8 += tok.z[c][j] >= least;
+          behind = lanes_reduce<LPT>(n8, [](uint32_t a, uint32_t b) { return a + b; }) > 8;
+        }
+        rounds = __ballot(tok.counts && (behind || close_among<false>(best, low, k))) != 0;      // uniform over the wave
         if (rounds) {                              // not with logits that have no such bits, as those that were BF16
           uint32_t bits = 0;
 #pragma unroll
           for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int j = 0; j < 8; ++j) bits |= __float_as_uint(tok.z[c][j]);
-          rounds = __ballot((bits & low) != 0) != 0;
+          rounds = __ballot((bits & low) != 0) != 0 && __ballot(tok.counts && (behind || close_among<true>(best, low, k))) != 0;
         }
       } else {
         best_eight<LPT, C>(key);

@@ -144,6 +144,21 @@ def test_moe_route_logits_close_to_each_other(e, k):
         _check_route(fp8q.moe_route(_place(part, F32), k), part.astype(np.float64), k, None, False)
 
 
+@pytest.mark.parametrize("e", [8, 60, 250, 1000])
+@pytest.mark.parametrize("k", [4, 5, 6, 7, 8])
+def test_moe_route_few_logits_left(e, k):
+    """FP32 logits close to each other and not, with all experts, a handful, one and none of them left by minus infinity."""
+    fp8q = require_gpu()
+    rng = np.random.default_rng(e * k)
+    z = np.concatenate([(np.float32(1.5).view(np.int32) + rng.integers(0, 4 * e, (90, e))).astype(np.int32).view(np.float32),
+                        _logits(90, e, F32, e + k)])
+    z[::7] = -z[::7]
+    for i, row in enumerate(z):
+        if i % 3:
+            row[rng.permutation(e)[i % 10:]] = -np.inf
+    _check_route(fp8q.moe_route(_place(z, F32), k, renormalize=True), z.astype(np.float64), k, None, True)
+
+
 @pytest.mark.parametrize("case", ["no tokens", "none valid", "all minus infinity"])
 def test_moe_route_where_no_token_counts(case):
     fp8q = require_gpu()
