@@ -120,6 +120,42 @@ def test_layer_on_a_stream_argument_alone(t):
         assert all(bool((x == 0x55).all()) for x in noise)
 
 
+@pytest.mark.parametrize("form", ["stream", "handle"])
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("t", [2, 300, 5000])
+def test_logits_gradient_on_a_stream_argument_alone(t, given, form):
+    """moe_route_backward with stream=s behind work of s that writes what it reads, into new and given outputs: the logits of
+    the layer with rows padded to 16 bytes, as the default stream gives it for them."""
+    fp8q = require_gpu()
+    args = _inputs(61, t)
+    layer = _layer(fp8q, *args)
+    z = torch.nn.functional.pad(_logits(layer[4], args[3]).contiguous(), (0, 2))[:, :E]
+    weights, experts, loss, slope = (layer[i] for i in (5, 6, 8, 9))
+    want = _bytes(fp8q.moe_route_backward(z, experts, slope, dweights=weights, dloss=loss, renormalize=True))
+    assert np.array_equal(want, _bytes(layer[14]))        # the layer's own logits lie in rows of 8
+    s = torch.cuda.Stream()
+    late = [torch.zeros_like(x) for x in (weights, slope, loss)]
+    zl, el = torch.zeros((t, 8), dtype=BF, device="cuda")[:, :E], torch.full_like(experts, -1)
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x in (zl, *late):
+            x.zero_()
+        out = torch.full((t, 8), 7.0, dtype=BF, device="cuda")[:, :E] if given else None
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            for _ in range(4):
+                busy = busy @ busy.t() * 1e-3
+            for x, y in zip((zl, el, *late), (z, experts, weights, slope, loss)):
+                x.copy_(y)
+        dz = fp8q.moe_route_backward(zl, el, late[1], dweights=late[0], dloss=late[2], renormalize=True, dlogits=out,
+                                     stream=s if form == "stream" else s.cuda_stream)
+        noise = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda") for n in (512, 4096, 1 << 16, 1 << 18)]
+        s.synchronize()
+        assert np.array_equal(_bytes(dz), want) and (not given or dz is out)
+        assert all(bool((x == 0x55).all()) for x in noise)
+
+
 @pytest.mark.parametrize("t", [1, 300, 5000])
 def test_layer_captured_in_a_hip_graph_and_replayed(t):
     """Two graphs of the layer on buffers of their own, replayed in turn with new inputs and eager work between: each has
