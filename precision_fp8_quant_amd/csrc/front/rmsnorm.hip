@@ -129,7 +129,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(NormArgs
 // Column maxima go over the thread's rows, the wave (permlane swaps) and the 8
 // waves (LDS); transposed codes are staged in LDS and leave 32 bytes a thread.
 // Rows past M are zeros.
-// Bound by memory: 8192x7168 BF16 41 us, 5.8 TB/s, after 56 us (6.3 TB/s) of the
+// Bound by memory: 8192x7168 BF16 41 us, 5.9 TB/s, after 55 us (6.4 TB/s) of the
 // kernel above with a residual.  It is a second kernel because a column's tile
 // needs the rstd of 128 rows, more than a CU holds; its read of h is what the two
 // passes pay for that, and comes out of the caches in part.
@@ -148,11 +148,12 @@ __global__ __launch_bounds__(512) void rmsnorm_dual_kernel(NormArgs p) {
   const int t = threadIdx.x, c16 = t & 15, rq = t >> 4;
   const int64_t cblocks = p.D >> 7, rblocks = (p.M + 127) >> 7, mp = rblocks << 7;
   for (int64_t u = blockIdx.x; u < cblocks * rblocks; u += gridDim.x) {   // block-uniform: barriers stay matched
-    // Backwards, four row blocks at a time: what the kernel before wrote last is still in the caches, and the four
-    // extend the same 512 bytes of q_t (both kernels 108 us; forwards by columns 116; with x and the residual past
-    // the caches, which keeps more of h in them, 91).
-    const int64_t left = rblocks - u / (4 * cblocks) * 4, high = left < 4 ? left : 4, v4 = u % (4 * cblocks);
-    const int64_t br = left - 1 - v4 % high, bc = v4 / high;
+    // Four row blocks at a time, which extend the same 512 bytes of q_t.  Measured (8192x7168 BF16, inputs from memory, with
+    // a residual / without, us a call that writes where the last one's dropped outputs were, and one whose last outputs are
+    // still held): 92.4 / 67.3 and 103.7 / 69.4; row by row 93.3 / 68.5 and 103.9 / 70.6, column by column 92.9 / 71.5 and
+    // 107.8 / 72.4; fours from the end, where h was written last, 92.7 / 68.1 and 106.6 / 73.0.
+    const int64_t first = u / (4 * cblocks) * 4, left = rblocks - first, high = left < 4 ? left : 4, v4 = u % (4 * cblocks);
+    const int64_t br = first + v4 % high, bc = v4 / high;
     const int64_t col = bc * 128 + c16 * 8, row0 = br * 128 + rq * 4;
     Row8<T> hr[4];
     Row8<W> wr;
