@@ -142,7 +142,13 @@ hipError_t launch_moe_dispatch(const DispatchArgs& p, hipStream_t st);
 // of 8 of 64, 7168 codes 18.0 / 19.8, 2048 codes 13.6 / 16.8; 1024 of 8 of 64, 7168
 // codes 40.1 / 29.0, 2048 codes 17.5 / 20.9).
 constexpr int64_t kDispatchOneLaunch = 4096;
-// Slots whose ranks one workgroup alone finds.
+// Slots whose ranks one workgroup alone finds: a launch less for the host, and one
+// CU's work (us a call and in a graph, alone / in two kernels: 4352 slots of 8 of 64
+// experts, 128 codes, 16.0 / 15.9 and 15.2 / 14.0, 2048 codes 18.2 / 18.2 and 18.0 /
+// 16.7; of 2 of 8, 128 codes, 14.5 / 16.4 and 13.9 / 13.7; 8192 slots of 8 of 64, 128
+// codes, 17.9 / 15.8 and 17.3 / 14.0, 7168 codes 30.3 / 27.5 and 30.6 / 27.4; of 8 of
+// 256, 2048 codes, 28.4 / 25.2 and 28.4 / 25.4).  It is ahead up to some 5000 slots
+// where the host is what a call waits for, and behind elsewhere.
 constexpr int64_t kDispatchAlone = 8192;
 
 // Slots of one wave, whole steps of 64, for up to 128 workgroups of 16 waves.

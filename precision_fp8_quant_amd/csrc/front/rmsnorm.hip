@@ -230,7 +230,8 @@ hipError_t launch_rows(const NormArgs& p, hipStream_t st) {
 
 // A row's threads by its width.  Measured (8192x7168 BF16 with a residual, FP8, us): 256 threads of 4 runs 78, 512 of 2
 // 83, 1024 of 1 106; 8192x2048: 256 of 1 22.8, 64 of 4 23.4; 65536x128: 16 lanes of 1 14.0, 64 29.8; 65536x256: 16 of 2
-// 21.6, 64 of 1 29.9.
+// 21.6, 64 of 1 29.9 (all alone; a call among others takes 11.7 and 19.9 of the last two, and 8.1 and 11.7 without a
+// residual, of which the vector units issue for 5.9 and 8.3).
 template <typename T, typename W, int OUT>
 hipError_t launch_out(const NormArgs& p, hipStream_t st) {
   if (p.D <= 128) return launch_rows<T, W, 16, 1, OUT>(p, st);

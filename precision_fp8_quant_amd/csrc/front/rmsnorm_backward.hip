@@ -7,10 +7,12 @@
 // 8 (i TPR + t)), and each thread keeps the sums of dw of its own columns over
 // all rows of its workgroup.  The workgroups' sums (in the workspace, one row
 // each) are added by a second kernel, in a fixed order: no atomics.
-// Bound by memory: 8192x7168 BF16 with dh 85 us, 5.5 TB/s (a large copy: 5.1), and 5
-// us for the sums.  The registers of the sums decide the shape: 1024 threads of one
-// run 91 us, 512 of two 93, 256 of four (one wave per SIMD) 107 with 256 workgroups
-// and the sums' kernel; 512 workgroups 93, 2048, with 59 MB of sums, 109.
+// Bound by memory: 8192x7168 BF16 with dh 83.6 us, 5.6 TB/s (a large copy: 5.1), and
+// with the sums 86.3 among calls like it; each alone under a profiler 85.2 and 5.0,
+// with the start and the end of a launch.  The registers of the sums decide the shape:
+// 1024 threads of one run 91 us, 512 of two 93, 256 of four (one wave per SIMD) 107
+// with 256 workgroups, both kernels alone; 512 workgroups 93, 2048, with 59 MB of
+// sums, 109.
 #include "front_launch.h"
 #include "lanes.h"
 #include "row_io.h"
@@ -24,7 +26,9 @@ __global__ __launch_bounds__(NT) void rmsnorm_backward_kernel(NormBwdArgs p) {
   constexpr int RPB = NT / TPR;                    // rows at a time
   // With four runs the registers hold no more than dy and h: the sums of dw are in LDS, each thread's its own.  In FP32
   // they hold dy alone, and h is read again from the caches.  (2048x32768 with dh, us: BF16 114, with the sums in
-  // registers, which spill, 194; FP32 343, with h in registers 390, the sums too 566.)
+  // registers, which spill, 194; FP32 343, with h in registers 390, the sums too 566.  With an FP32 weight the BF16 form
+  // still spills 6 registers, 138; FP32 30.  With two runs FP32 spills 4 with a BF16 weight alone: 4096x16384 225, with an
+  // FP32 one 213.)
   constexpr bool LATE = R > 2;
   constexpr bool AGAIN = LATE && sizeof(T) == 4;
   __shared__ v4f far[LATE ? 2 * R : 1][LATE ? TPR : 1];
@@ -173,7 +177,7 @@ hipError_t launch(const NormBwdArgs& p, hipStream_t st) {
   int64_t parts = norm_bwd_parts(p.M, p.D);        // which counts on the rows of a workgroup here
   // BF16 rows of 1025 to 2048 channels, more than 512 of them: four at a time, in a quarter of the workgroups (with dh,
   // us in a graph, four / one: 1511x2048 9.7 / 11.4, 8192x2048 25.6 / 27.5, 32768x1536 78 / 93; 128x2048 5.7 / 5.2;
-  // FP32 1511x2048 13.3 / 14.5, 8192x2048 55.9 / 52.7, 32768x2048 198 / 188).
+  // FP32, which has one everywhere, 1511x2048 13.3 / 14.5, 8192x2048 55.9 / 52.7, 32768x2048 198 / 188).
   const bool four = sizeof(T) == 2 && p.D > 1024 && p.D <= 2048 && p.M > 512;
   if (four) parts = p.M < 1024 ? (p.M + 3) / 4 : 256;   // never more than norm_bwd_parts says
   if (parts > 0) {

@@ -16,17 +16,22 @@
 //   any number      rounds: every lane sorts its runs with all their bits, each of
 //                   the k rounds takes the largest of their heads over the lanes and
 //                   moves that run up.
-// (65536 tokens, merged / by rounds, us: 8 of 64 BF16 9.7 / 11.9, FP32 12.2 / 13.7,
-// 8 of 256 FP32 28.5 / 32.5, 8 of 1000 (16384) 31.2 / 34.8, 4 of 64 BF16 9.2 / 9.6;
-// 2 of 64 a call 12.5 / 12.1, 2 of 1000 34.1 / 31.7.)
+// (65536 tokens, merged / by rounds, us: 8 of 64 BF16 9.7 / 11.9, FP32 11.9 / 13.7,
+// 8 of 256 FP32 26.3 / 32.5, 8 of 1000 (16384) 31.1 / 34.8, 4 of 64 BF16 9.1 / 9.6;
+// 2 of 64 a call 12.5 / 12.1, 2 of 1000 34.1 / 31.7.  16 of 64 BF16 by rounds 13.8,
+// 16 of 256 FP32 40.7.)
 //
 // A lane has the same 8 C experts in all of its workgroup's tokens and sums
 // their p in registers, a wave its groups', a workgroup its waves'; workgroups
 // leave one row of sums and counts each, which a second kernel adds in a fixed
 // order.  With one workgroup it is all one launch.
-// Bound by instructions, half of them the choice (6 us of the 9.7 are without it),
-// and 3.8 us for the sums.  The gradient is bound by memory: 8 of 256 FP32 27.5 us a
-// call, 5.0 TB/s, 8 of 1000 (16384 tokens) 26.5, 5.0.
+// Bound by the vector units, which issue for 5.2 us of the 9.7 (8 of 64 BF16; 6 us
+// are without the choice), 17.4 of 26.3 (8 of 256 FP32) and 35.5 of 40.7 (16 of 256
+// by rounds), and by a launch's start and end and the loads of a turn, that nothing
+// hides; then 3.9 us for the sums.  The gradient is bound by memory: 8 of 256 FP32
+// 27.5 us a call, 5.0 TB/s, 8 of 1000 (16384 tokens) 26.5, 5.0; BF16 with fewer
+// experts by both (8 of 64, 65536 tokens, 8.1 us a call, 4.4 of them vector
+// instructions; 8 of 128 11.0 and 8.0).
 #include "front_launch.h"
 #include "lanes.h"
 #include "route_choice.h"
